@@ -55,6 +55,36 @@ class c_li_query(ctypes.Structure):
                 ("H", ctypes.c_int32), ("q_pos", ctypes.c_void_p)]
 
 
+class c_li_row_transform(ctypes.Structure):
+    _fields_ = [("norm", ctypes.c_int), ("norm_offset", ctypes.c_int32), ("norm_dim", ctypes.c_int32),
+                ("gamma", ctypes.c_void_p), ("beta", ctypes.c_void_p), ("eps", ctypes.c_float),
+                ("rope_offset", ctypes.c_int32), ("rope_dim", ctypes.c_int32), ("rope_halves", ctypes.c_int32),
+                ("inv_freq", ctypes.c_void_p)]
+
+
+class c_li_head_rows(ctypes.Structure):
+    _fields_ = [("x", ctypes.c_void_p), ("out", ctypes.c_void_p), ("H", ctypes.c_int32), ("dim", ctypes.c_int32),
+                ("tok_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64), ("out_tok_stride", ctypes.c_int64),
+                ("out_head_stride", ctypes.c_int64), ("tf", c_li_row_transform)]
+
+
+class c_li_paged_cache(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("page_table", ctypes.c_void_p), ("lengths", ctypes.c_void_p),
+                ("batch", ctypes.c_int32), ("n_pages", ctypes.c_int32), ("page_size", ctypes.c_int32),
+                ("max_pages", ctypes.c_int32), ("dim", ctypes.c_int32), ("dtype", ctypes.c_int)]
+
+
+class c_li_prompt(ctypes.Structure):
+    _fields_ = [("q", ctypes.c_void_p), ("k_nope", ctypes.c_void_p), ("k_rope", ctypes.c_void_p),
+                ("v", ctypes.c_void_p), ("dtype", ctypes.c_int), ("H", ctypes.c_int32), ("d_nope", ctypes.c_int32),
+                ("d_rope", ctypes.c_int32), ("d_v", ctypes.c_int32), ("total_q", ctypes.c_int32),
+                ("total_k", ctypes.c_int32), ("batch", ctypes.c_int32), ("max_q", ctypes.c_int32),
+                ("q_tok_stride", ctypes.c_int64), ("q_head_stride", ctypes.c_int64), ("k_tok_stride", ctypes.c_int64),
+                ("k_head_stride", ctypes.c_int64), ("kr_tok_stride", ctypes.c_int64), ("v_tok_stride", ctypes.c_int64),
+                ("v_head_stride", ctypes.c_int64), ("cu_q", ctypes.c_void_p), ("cu_k", ctypes.c_void_p),
+                ("scale", ctypes.c_float), ("causal", ctypes.c_int32)]
+
+
 class c_li_profile_record(ctypes.Structure):
     _fields_ = [("kernel", ctypes.c_char * 48), ("ms", ctypes.c_float), ("grid", ctypes.c_int32),
                 ("block", ctypes.c_int32), ("smem", ctypes.c_int32)]
@@ -90,6 +120,13 @@ _sigs = {
     "li_topk": (_I, [_P, _P, _I, _I, _I64, _P, _I, _P, _P, _P, _SZ, _P]),
     "li_recall_workspace_bytes": (_SZ, [_P, _I, _I, _I, _I]),
     "li_attention_recall": (_I, [_P, _P, _I, _I, _I, _P, _P, _I, _I, _P, _P, _P, _SZ, _P]),
+    "li_attention_workspace_bytes": (_SZ, [_P, _I, _I]),
+    "li_norm_rope": (_I, [_P, ctypes.POINTER(c_li_head_rows), _I, _I, _I64, _P, _P]),
+    "li_append_paged": (_I, [_P, ctypes.POINTER(c_li_paged_cache), _P, _I, _I64, ctypes.POINTER(c_li_row_transform), _P,
+                             _P, _P, _SZ, _P]),
+    "li_latent_attention": (_I, [_P, ctypes.POINTER(c_li_paged_cache), _P, _I, _I, _I, ctypes.c_float, _P, _P, _I, _P,
+                                 _P, _P, _SZ, _P]),
+    "li_prompt_attention": (_I, [_P, ctypes.POINTER(c_li_prompt), _P, _P, _P, _SZ, _P]),
     "li_set_trace": (_I, [_P, _P, _SZ]),
     "li_profile_enable": (_I, [_P, _I]),
     "li_profile_read": (_I, [_P, ctypes.POINTER(c_li_profile_record), _I, ctypes.POINTER(_I)]),
@@ -348,6 +385,194 @@ def li_attention_recall(ctx: Context, probs: torch.Tensor, sel: torch.Tensor, K:
     ctx.check(_lib.li_attention_recall(ctx.handle, _ptr(probs), rows, H, N, _ptr(lengths), _ptr(sel), int(k), int(K),
                                        _ptr(rec), _ptr(mrec), _ptr(ws), ws.numel(), _stream(stream)))
     return rec, mrec
+
+
+# ---------------------------------------------------------------- attention over the selected tokens
+
+_NORM = {"none": 0, "rms": 1, "layer": 2}
+
+
+def _need(ok: bool, status: str, message: str):
+    """Shape and type checks of the tensors behind the pointers, which the C entry points cannot see."""
+    if not ok:
+        raise LiError(STATUS[status], message)
+
+
+def _check_tensor(name: str, t: Optional[torch.Tensor], shape, dtype, ctx: Context, contiguous: bool = True):
+    if t is None:
+        return
+    _need(tuple(t.shape) == tuple(shape), "LI_ERR_SHAPE", f"{name} is {tuple(t.shape)}, expected {tuple(shape)}")
+    _need(t.dtype == dtype, "LI_ERR_DTYPE", f"{name} is {t.dtype}, expected {dtype}")
+    _need(t.device.type != "cuda" or t.device.index == ctx.device, "LI_ERR_ARG",
+          f"{name} is on {t.device}, the context on device {ctx.device}")
+    _need(t.is_contiguous() if contiguous else t.shape[-1] <= 1 or t.stride(-1) == 1, "LI_ERR_ARG",
+          f"{name} must be contiguous" if contiguous else f"rows of {name} must be contiguous")
+
+
+@dataclass
+class RowTransform:
+    """Transforms of one row (li_row_transform): a norm ("none", "rms" or
+    "layer") of elements [norm_offset, norm_offset + norm_dim) with optional
+    gamma / beta [norm_dim] float32, then the rotation of [rope_offset,
+    rope_offset + rope_dim) by inv_freq [rope_dim / 2] float32, slots being
+    adjacent pairs or, with rope_halves, element p and p + rope_dim / 2."""
+    norm: str = "none"
+    norm_offset: int = 0
+    norm_dim: int = 0
+    gamma: Optional[torch.Tensor] = None
+    beta: Optional[torch.Tensor] = None
+    eps: float = 1e-6
+    rope_offset: int = 0
+    rope_dim: int = 0
+    rope_halves: bool = False
+    inv_freq: Optional[torch.Tensor] = None
+
+    def c(self, ctx: Context) -> c_li_row_transform:
+        _need(self.norm in _NORM, "LI_ERR_ARG", f"unknown norm {self.norm!r}")
+        for name in ("gamma", "beta"):
+            _check_tensor(name, getattr(self, name), (self.norm_dim,), torch.float32, ctx)
+        if self.rope_dim:
+            _check_tensor("inv_freq", self.inv_freq, (self.rope_dim // 2,), torch.float32, ctx)
+        return c_li_row_transform(_NORM[self.norm], self.norm_offset, self.norm_dim, _ptr(self.gamma), _ptr(self.beta),
+                                  float(self.eps), self.rope_offset, self.rope_dim, 1 if self.rope_halves else 0,
+                                  _ptr(self.inv_freq))
+
+
+@dataclass
+class HeadRows:
+    """The heads of every token in one tensor (li_head_rows): x [n_tok, H,
+    dim] and out of the same shape, any strides over tokens and heads; out
+    may be x."""
+    x: torch.Tensor
+    tf: RowTransform
+    out: torch.Tensor
+
+    def c(self, ctx: Context) -> c_li_head_rows:
+        _need(self.x.dim() == 3, "LI_ERR_SHAPE", f"x is {tuple(self.x.shape)}, expected [n_tok, H, dim]")
+        n, H, dim = self.x.shape
+        _check_tensor("x", self.x, (n, H, dim), self.x.dtype, ctx, contiguous=False)
+        _check_tensor("out", self.out, (n, H, dim), self.x.dtype, ctx, contiguous=False)
+        return c_li_head_rows(_ptr(self.x), _ptr(self.out), H, dim, self.x.stride(0), self.x.stride(1),
+                              self.out.stride(0), self.out.stride(1), self.tf.c(ctx))
+
+
+@dataclass
+class PagedCache:
+    """A paged cache of attention latents (li_paged_cache): data [n_pages,
+    page_size, dim] float32 or bfloat16, page_table [batch, max_pages] int32,
+    lengths [batch] int32."""
+    data: torch.Tensor
+    page_table: torch.Tensor
+    lengths: torch.Tensor
+
+    def c(self, ctx: Context) -> c_li_paged_cache:
+        _need(self.data.dim() == 3 and self.page_table.dim() == 2, "LI_ERR_SHAPE",
+              "data must be [n_pages, page_size, dim] and page_table [batch, max_pages]")
+        (n_pages, page, dim), (batch, max_pages) = self.data.shape, self.page_table.shape
+        _check_tensor("data", self.data, (n_pages, page, dim), self.data.dtype, ctx)
+        _check_tensor("page_table", self.page_table, (batch, max_pages), torch.int32, ctx)
+        _check_tensor("lengths", self.lengths, (batch,), torch.int32, ctx)
+        return c_li_paged_cache(_ptr(self.data), _ptr(self.page_table), _ptr(self.lengths), batch, n_pages, page,
+                                max_pages, dim, _attn_dtype(self.data))
+
+
+def _attn_dtype(t: torch.Tensor) -> int:
+    _need(t.dtype in (torch.float32, torch.bfloat16), "LI_ERR_DTYPE", f"float32 or bfloat16 only (got {t.dtype})")
+    return _DTYPE_CODE[t.dtype]
+
+
+def li_attention_workspace_bytes(ctx: Optional[Context], H: int, d_v: int) -> int:
+    return int(_lib.li_attention_workspace_bytes(ctx.handle if ctx else None, int(H), int(d_v)))
+
+
+def attention_workspace(ctx: Context, H: int, d_v: int, device=None) -> torch.Tensor:
+    """A zero-filled workspace of li_attention_workspace_bytes(...) bytes: for
+    li_append_paged, li_latent_attention and li_prompt_attention of up to H
+    heads of d_v values."""
+    return torch.zeros(li_attention_workspace_bytes(ctx, H, d_v), dtype=torch.uint8, device=device or f"cuda:{ctx.device}")
+
+
+def li_norm_rope(ctx: Context, sets: List[HeadRows], pos: Optional[torch.Tensor] = None, stream=None):
+    """Norms and rotation of the heads in every tensor of `sets` (1 to 4, the
+    same tokens and type), pos [n_tok] int32, in one launch."""
+    _need(1 <= len(sets) <= 4, "LI_ERR_ARG", f"need 1 to 4 tensors (got {len(sets)})")
+    n = sets[0].x.shape[0]
+    for s in sets:
+        _need(s.x.shape[0] == n and s.x.dtype == sets[0].x.dtype, "LI_ERR_SHAPE", "the tensors differ in tokens or type")
+    _check_tensor("pos", pos, (n,), torch.int32, ctx)
+    arr = (c_li_head_rows * len(sets))(*[s.c(ctx) for s in sets])
+    ctx.check(_lib.li_norm_rope(ctx.handle, arr, len(sets), _attn_dtype(sets[0].x), n, _ptr(pos), _stream(stream)))
+
+
+def li_append_paged(ctx: Context, cache: PagedCache, x: torch.Tensor, ws: torch.Tensor, tf: Optional[RowTransform] = None,
+                    start: Optional[torch.Tensor] = None, n_new: Optional[torch.Tensor] = None, stream=None):
+    """x [batch, T, dim] (rows at one stride) into the cache, transformed, at
+    positions start[b] (or lengths[b]) onwards; n_new [batch]: rows of each
+    sequence."""
+    cc = cache.c(ctx)
+    _need(x.dim() == 3, "LI_ERR_SHAPE", f"x is {tuple(x.shape)}, expected [batch, T, dim]")
+    T = x.shape[1]
+    _check_tensor("x", x, (cc.batch, T, cc.dim), cache.data.dtype, ctx, contiguous=False)
+    stride = x.stride(1) if T > 1 else x.stride(0)
+    _need(cc.batch == 1 or T == 0 or x.stride(0) == T * stride, "LI_ERR_ARG", "the rows of x must lie at one stride")
+    _check_tensor("start", start, (cc.batch,), torch.int32, ctx)
+    _check_tensor("n_new", n_new, (cc.batch,), torch.int32, ctx)
+    ct = tf.c(ctx) if tf is not None else None
+    ctx.check(_lib.li_append_paged(ctx.handle, ctypes.byref(cc), _ptr(x), T, stride,
+                                   ctypes.byref(ct) if ct is not None else None, _ptr(start), _ptr(n_new), _ptr(ws),
+                                   ws.numel(), _stream(stream)))
+
+
+def li_latent_attention(ctx: Context, cache: PagedCache, q: torch.Tensor, d_v: int, scale: float, out: torch.Tensor,
+                        ws: torch.Tensor, lse: Optional[torch.Tensor] = None, sel: Optional[torch.Tensor] = None,
+                        q_pos: Optional[torch.Tensor] = None, stream=None):
+    """Absorbed queries q [batch, T, H, dim] over the cached latents: the
+    positions of sel [batch, T, k] (a selection output), or the whole prefix.
+    out [batch, T, H, d_v], lse [batch, T, H] float32, q_pos [batch, T]."""
+    cc = cache.c(ctx)
+    _need(q.dim() == 4, "LI_ERR_SHAPE", f"q is {tuple(q.shape)}, expected [batch, T, H, dim]")
+    _, T, H, _ = q.shape
+    dt = cache.data.dtype
+    _check_tensor("q", q, (cc.batch, T, H, cc.dim), dt, ctx)
+    _check_tensor("out", out, (cc.batch, T, H, d_v), dt, ctx)
+    _check_tensor("lse", lse, (cc.batch, T, H), torch.float32, ctx)
+    _check_tensor("q_pos", q_pos, (cc.batch, T), torch.int32, ctx)
+    k = 0
+    if sel is not None:
+        k = sel.shape[-1]
+        _need(k >= 1, "LI_ERR_SHAPE", "k must be >= 1 with sel")
+        _check_tensor("sel", sel, (cc.batch, T, k), torch.int32, ctx)
+    ctx.check(_lib.li_latent_attention(ctx.handle, ctypes.byref(cc), _ptr(q), T, H, int(d_v), float(scale), _ptr(q_pos),
+                                       _ptr(sel), k, _ptr(out), _ptr(lse), _ptr(ws), ws.numel(), _stream(stream)))
+
+
+def li_prompt_attention(ctx: Context, q: torch.Tensor, k_nope: torch.Tensor, k_rope: Optional[torch.Tensor],
+                        v: torch.Tensor, cu_q: torch.Tensor, cu_k: torch.Tensor, max_q: int, scale: float,
+                        out: torch.Tensor, ws: torch.Tensor, lse: Optional[torch.Tensor] = None, causal: bool = True,
+                        stream=None):
+    """Expanded attention of a ragged batch of prompts: q [total_q, H, d_nope +
+    d_rope], k_nope [total_k, H, d_nope], k_rope [total_k, d_rope] (shared by
+    the heads) or None, v [total_k, H, d_v], any strides over tokens and
+    heads; cu_q, cu_k [batch + 1] int32; out [total_q, H, d_v], lse
+    [total_q, H] float32."""
+    _need(q.dim() == 3 and k_nope.dim() == 3 and v.dim() == 3, "LI_ERR_SHAPE", "q, k_nope and v must be [tokens, H, dim]")
+    (tq, H, dq), (tk, _, dn), dv = q.shape, k_nope.shape, v.shape[-1]
+    dr = 0 if k_rope is None else k_rope.shape[-1]
+    batch = cu_q.numel() - 1
+    _check_tensor("q", q, (tq, H, dn + dr), q.dtype, ctx, contiguous=False)
+    _check_tensor("k_nope", k_nope, (tk, H, dn), q.dtype, ctx, contiguous=False)
+    _check_tensor("k_rope", k_rope, (tk, dr), q.dtype, ctx, contiguous=False)
+    _check_tensor("v", v, (tk, H, dv), q.dtype, ctx, contiguous=False)
+    _check_tensor("cu_q", cu_q, (batch + 1,), torch.int32, ctx)
+    _check_tensor("cu_k", cu_k, (batch + 1,), torch.int32, ctx)
+    _check_tensor("out", out, (tq, H, dv), q.dtype, ctx)
+    _check_tensor("lse", lse, (tq, H), torch.float32, ctx)
+    p = c_li_prompt(_ptr(q), _ptr(k_nope), _ptr(k_rope), _ptr(v), _attn_dtype(q), H, dn, dr, dv, tq, tk, batch, int(max_q),
+                    q.stride(0), q.stride(1), k_nope.stride(0), k_nope.stride(1),
+                    0 if k_rope is None else k_rope.stride(0), v.stride(0), v.stride(1), _ptr(cu_q), _ptr(cu_k),
+                    float(scale), 1 if causal else 0)
+    ctx.check(_lib.li_prompt_attention(ctx.handle, ctypes.byref(p), _ptr(out), _ptr(lse), _ptr(ws), ws.numel(),
+                                       _stream(stream)))
 
 
 def li_set_trace(ctx: Context, buf: Optional[torch.Tensor]):

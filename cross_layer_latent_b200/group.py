@@ -14,9 +14,10 @@ from typing import List, Optional
 
 import torch
 
-from ._binding import (LI_BF16, LI_E4M3, LI_F32, Cache, Context, LatentTransform, Query, li_absorb_query,
-                       li_absorb_query_group, li_append_latent, li_append_latent_ex, li_dsa_score_topk,
-                       li_hs_anchor_candidates, li_hs_follower_refine, li_score_topk, workspace)
+from ._binding import (LI_BF16, LI_E4M3, LI_F32, Cache, Context, LatentTransform, PagedCache, Query,
+                       attention_workspace, li_absorb_query, li_absorb_query_group, li_append_latent,
+                       li_append_latent_ex, li_attention_workspace_bytes, li_dsa_score_topk, li_hs_anchor_candidates,
+                       li_hs_follower_refine, li_latent_attention, li_score_topk, workspace)
 
 TORCH_DTYPE = {LI_F32: torch.float32, LI_BF16: torch.bfloat16, LI_E4M3: torch.uint8}
 
@@ -194,6 +195,21 @@ class GroupIndexer:
         li_dsa_score_topk(self.ctx, self.keys[layer], self.raw_query(layer), self.k, self.idx[layer],
                           self.score[layer], dump, self.ws, stream)
         return self.idx[layer]
+
+    # ------------------------------------------------------------ attention over the selection
+    def attend(self, layer: int, cache: PagedCache, q: torch.Tensor, d_v: int, scale: float, out: torch.Tensor,
+               lse: Optional[torch.Tensor] = None, stream=None):
+        """The layer's latent attention over the tokens it selected last
+        (idx[layer]): absorbed queries q [batch, T, heads, dim] over the layer's
+        own paged latents, out [batch, T, heads, d_v].  The heads are the
+        attention's, not the indexer's.  Its workspace is made by the first
+        call (make that call before any capture) and grows with the heads."""
+        need = li_attention_workspace_bytes(self.ctx, q.shape[2], d_v)
+        if not hasattr(self, "ws_attn") or self.ws_attn.numel() < need:
+            self.ws_attn = attention_workspace(self.ctx, q.shape[2], d_v, device=self.device)
+        li_latent_attention(self.ctx, cache, q, d_v, scale, out, self.ws_attn, lse=lse, sel=self.idx[layer],
+                            q_pos=self.q_pos, stream=stream)
+        return out
 
     def hs_step(self, stream=None):
         """One HS decode step of the group: anchor proposes, followers refine."""

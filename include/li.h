@@ -383,6 +383,190 @@ LI_API li_status li_topk(li_ctx* ctx, const float* scores, int rows, int n, int6
                   const int32_t* lengths, int k, int32_t* out_idx, float* out_score, void* ws,
                   size_t ws_bytes, void* stream);
 
+/* --------------------------------------- attention over the selected tokens */
+
+/* The operators around a layer's attention itself: what reads the
+ * selections above.  They are written from the usual definitions (RMS norm,
+ * rotary positions, softmax attention with one latent vector a token as key
+ * and value); the LatentIndex summary takes them as given (Sec. 4.1: the
+ * selected tokens are what the sparse attention reads).
+ * Shared rules:
+ *  - F32 and BF16 only, one type per call; sums, norms, softmax statistics
+ *    and accumulators are fp32.
+ *  - The context's device must be the current device (LI_ERR_ARG).
+ *  - `ws` is a workspace as under "Memory", of at least
+ *    li_attention_workspace_bytes(...) bytes (li_workspace_bytes never
+ *    serves here); two calls that share one must be ordered on the GPU, so
+ *    graphs that may replay at the same time need one each.                */
+
+typedef enum { LI_NORM_NONE = 0, LI_NORM_RMS = 1, LI_NORM_LAYER = 2 } li_norm;
+
+/* Transforms of one row x of `dim` elements, the norm first, then the
+ * rotation (the ranges may overlap: a norm over the whole head, its last part
+ * rotated).
+ * Norm: elements [norm_offset, norm_offset + norm_dim) become, in fp32,
+ *   RMS    x / sqrt(mean(x^2) + eps) * gamma + beta
+ *   LAYER  (x - mean) / sqrt(var + eps) * gamma + beta  (biased variance)
+ *   gamma, beta: [norm_dim] fp32 device arrays, NULL for 1 and 0.
+ * Rotation: elements [rope_offset, rope_offset + rope_dim) hold rope_dim / 2
+ *   complex slots; slot p turns by position * inv_freq[p] (inv_freq
+ *   [rope_dim / 2] fp32, device): x' = x cos - y sin, y' = x sin + y cos.
+ *   Slot p is (x[2p], x[2p+1]) with rope_halves = 0, the layout of
+ *   li_append_latent_ex, and (x[p], x[p + rope_dim / 2]) with rope_halves = 1.
+ *   The angle is formed and reduced to a turn in double precision.
+ * norm = LI_NORM_NONE and rope_dim = 0 switch the parts off.                */
+typedef struct {
+  li_norm norm;
+  int32_t norm_offset;
+  int32_t norm_dim;
+  const float* gamma;
+  const float* beta;
+  float eps;
+  int32_t rope_offset;
+  int32_t rope_dim;
+  int32_t rope_halves;
+  const float* inv_freq;
+} li_row_transform;
+
+/* The heads of every token in one tensor: head h of token t is the row
+ * x + t * tok_stride + h * head_stride (elements; the row is contiguous),
+ * its result goes to out + t * out_tok_stride + h * out_head_stride.  Strides
+ * may be any whole numbers, negative ones too; rows of one output must not
+ * overlap, and an output may be its own input (in place: same address and
+ * strides) but must not overlap any input otherwise.                        */
+typedef struct {
+  const void* x;
+  void* out;
+  int32_t H;
+  int32_t dim;
+  int64_t tok_stride, head_stride;
+  int64_t out_tok_stride, out_head_stride;
+  li_row_transform tf;
+} li_head_rows;
+
+/* Norms of query and key heads with the position rotation in the same pass:
+ * the n_sets (1..4) tensors (a layer's queries, keys, indexer queries, ...)
+ * of the same n_tok tokens, in one launch.  pos [n_tok] int32 device
+ * positions, NULL if nothing is rotated.  dim 1..1024.  n_tok = 0 does
+ * nothing.  Everything may have any element alignment; rows whose addresses,
+ * strides and ranges are multiples of 8 elements (16 bytes) take wide loads. */
+LI_API li_status li_norm_rope(li_ctx* ctx, const li_head_rows* sets, int n_sets, li_dtype dtype, int64_t n_tok,
+                       const int32_t* pos, void* stream);
+
+/* A paged cache of attention latents: a pool of pages of page_size rows of
+ * `dim` elements; position s of sequence b is row s % page_size of page
+ * page_table[b][s / page_size].
+ * data       [n_pages][page_size][dim], 16-byte aligned; dim * element size
+ *            a multiple of 16; n_pages * page_size < 2^31.
+ * page_table [batch][max_pages] int32 device; entries of pages past a
+ *            sequence's length are never read.
+ * lengths    [batch] int32 device, valid positions per sequence (taken as
+ *            clamped to [0, max_pages * page_size], which is < 2^31).
+ * dtype      LI_F32 or LI_BF16.                                            */
+typedef struct {
+  void* data;
+  const int32_t* page_table;
+  int32_t* lengths;
+  int32_t batch;
+  int32_t n_pages;
+  int32_t page_size;
+  int32_t max_pages;
+  int32_t dim;
+  li_dtype dtype;
+} li_paged_cache;
+
+/* Bytes of workspace for li_append_paged, li_latent_attention and
+ * li_prompt_attention on this context, for up to H heads of d_v values.
+ * Independent of batch and lengths.  0 for invalid sizes.                   */
+LI_API size_t li_attention_workspace_bytes(const li_ctx* ctx, int H, int d_v);
+
+/* Append rows to a paged cache with their transforms on the way: for every
+ * sequence b and t < n_b, row tf(x[b][t]) is stored at position s_b + t (the
+ * position its rotation uses), then lengths[b] = s_b + n_b.
+ * x      [batch][T][cache->dim] of the cache's dtype, token (b, t) at
+ *        x + (b * T + t) * tok_stride elements (16-byte aligned rows).
+ * tf     NULL stores the rows as they are.
+ * start  [batch] int32 device: s_b (rewriting positions after a rejected
+ *        draft, say), or NULL: s_b = lengths[b].
+ * n_new  [batch] int32 device: n_b, clamped to [0, T] (padded batches), or
+ *        NULL: n_b = T.
+ * If s_b < 0 or s_b + n_b exceeds max_pages * page_size nothing is written
+ * for b, lengths[b] stays, and the status word records LI_ERR_CAPACITY.  A
+ * row whose page is outside [0, n_pages) is not written (LI_ERR_INDEX).
+ * Rows of sequences that share a page at the same offset are the caller's
+ * error.  dim at most 1024; needs batch * T < 2^31.                         */
+LI_API li_status li_append_paged(li_ctx* ctx, const li_paged_cache* cache, const void* x, int T, int64_t tok_stride,
+                          const li_row_transform* tf, const int32_t* start, const int32_t* n_new, void* ws,
+                          size_t ws_bytes, void* stream);
+
+/* Latent attention in absorbed form: every head of a token reads the same
+ * latent row c_s, whole as key and its first d_v elements as value.  For
+ * sequence b, query t, head h, over the positions s that it attends,
+ *   z_s = scale * (q[b][t][h] . c_s),  p = softmax(z),
+ *   out[b][t][h] = sum_s p_s c_s[0 .. d_v),  lse = log(sum_s exp z_s)
+ * (q = the query with the key expansion absorbed, its rotary part last; the
+ * value expansion is applied to out by the caller).
+ * Attended positions: n_bt = lengths[b], with q_pos min(lengths[b],
+ * q_pos[b][t] + 1).
+ *   sel NULL: all s in [0, n_bt).
+ *   sel [batch][T][k] int32 (a selection output, -1 padded): its entries in
+ *   [0, n_bt); negative ones are skipped, others record LI_ERR_INDEX and
+ *   are skipped.  A position listed twice counts twice.
+ * A query that attends nothing gets out = 0 and lse = -inf.  A page outside
+ * [0, n_pages) records LI_ERR_INDEX and its positions are skipped.  Rows
+ * that no query attends are not read (they may hold anything); without sel,
+ * rows below lengths[b] must be finite even where q_pos hides them from
+ * some of the T queries.
+ * q    [batch][T][H][cache->dim] of the cache's dtype, contiguous, 16-byte
+ *      aligned.  cache->dim <= 576, d_v in [1, min(dim, 512)].
+ * out  [batch][T][H][d_v] of the cache's dtype, contiguous.
+ * lse  [batch][T][H] fp32 or NULL.
+ * BF16 runs on the tensor cores: the weights p are rounded to bf16 before
+ * the product with the values, their sum is not.  Results do not depend on
+ * the order in which the GPU runs the parts.                                */
+LI_API li_status li_latent_attention(li_ctx* ctx, const li_paged_cache* cache, const void* q, int T, int H, int d_v,
+                              float scale, const int32_t* q_pos, const int32_t* sel, int k, void* out, float* lse,
+                              void* ws, size_t ws_bytes, void* stream);
+
+/* Latent attention in expanded form, for prompts: head h of key token j has
+ * the key (k_nope[j][h], k_rope[j]) -- the rotary part is shared by the heads
+ * -- and the value v[j][h].  The batch is ragged: sequence b has queries
+ * [cu_q[b], cu_q[b+1]) and keys [cu_k[b], cu_k[b+1]).  Query i of nq attends
+ * the keys j <= i + nk - nq with causal != 0 (the last query sees all nk
+ * keys), all nk keys without; scale, out and lse as li_latent_attention (a
+ * query that attends nothing: 0 and -inf).
+ * Strides are in elements, every row 16-byte aligned; a token's row of a
+ * head is contiguous.  q rows hold d_nope + d_rope elements.
+ * cu_q, cu_k [batch + 1] int32 device, non-decreasing from 0; values are
+ * clamped to [0, total_q] and [0, total_k], and rows of out and lse outside
+ * [cu_q[0], cu_q[batch]) are left as they were.  max_q: at least the longest
+ * sequence's queries (rows past max_q of a sequence are left as they were).
+ * k_rope NULL with d_rope 0.
+ * d_nope 1..128, d_rope 0..64, d_v 1..128, each times the element size a
+ * multiple of 16 bytes; total_q * H < 2^31.                                 */
+typedef struct {
+  const void* q;
+  const void* k_nope;
+  const void* k_rope;
+  const void* v;
+  li_dtype dtype;
+  int32_t H, d_nope, d_rope, d_v;
+  int32_t total_q, total_k, batch, max_q;
+  int64_t q_tok_stride, q_head_stride;
+  int64_t k_tok_stride, k_head_stride;
+  int64_t kr_tok_stride;
+  int64_t v_tok_stride, v_head_stride;
+  const int32_t* cu_q;
+  const int32_t* cu_k;
+  float scale;
+  int32_t causal;
+} li_prompt;
+
+/* out [total_q][H][d_v] of p->dtype, contiguous, 16-byte aligned; lse
+ * [total_q][H] fp32 or NULL. */
+LI_API li_status li_prompt_attention(li_ctx* ctx, const li_prompt* p, void* out, float* lse, void* ws, size_t ws_bytes,
+                              void* stream);
+
 /* ------------------------------------------------------ selection quality */
 
 /* Attention-mass recall of a selection (Sec. 4.1 and Table 1; Sec. D.3:
