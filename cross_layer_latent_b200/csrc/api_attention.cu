@@ -185,6 +185,66 @@ li_status append_paged(li_ctx* c, const li_paged_cache* cache, const void* x, in
   return e == cudaSuccess ? LI_OK : cuda_fail(c, e, "append_paged launch");
 }
 
+li_status latent_mma(li_ctx* c, const li_paged_cache* cache, const void* q, int T, int H, int d_v, float scale,
+                     const int32_t* q_pos, const int32_t* sel, int k, void* out, float* lse, void* ws, cudaStream_t st) {
+  const char* what = "li_latent_attention";
+  LatentMmaArgs a;
+  memset(&a, 0, sizeof(a));
+  a.page_table = cache->page_table;
+  a.lengths = cache->lengths;
+  a.q_pos = q_pos;
+  a.sel = sel;
+  a.out = out;
+  a.lse = lse;
+  a.status = at<int>(ws, 0);
+  a.part_ml = at<float>(ws, kAttnHeader);
+  a.part_o = a.part_ml + static_cast<size_t>(c->num_sms) * 2 * 64 * 2;
+  a.part_stride = latent_part_stride(d_v);
+  a.wait_ns = c->wait_ns;
+  a.scale_log2 = scale * 1.44269504089f;
+  a.seqs = sel ? cache->batch * T : cache->batch;
+  a.rows = sel ? H : T * H;
+  a.T = T;
+  a.H = H;
+  a.k = k;
+  a.dim = cache->dim;
+  a.d_v = d_v;
+  a.n_pages = cache->n_pages;
+  a.page_size = cache->page_size;
+  a.max_pages = cache->max_pages;
+  a.pool_rows = cache->n_pages * cache->page_size;
+  // whole boxes of rows where pages hold them (the 128-byte swizzle repeats every 8 rows)
+  a.box = 32;
+  while (cache->page_size % a.box) a.box /= 2;
+  if (a.box < 8) a.box = 0;
+  if (!latent_mma_layout(&a, c->num_sms, c->max_smem_optin))
+    return fail(c, LI_ERR_UNSUPPORTED, "%s: operands too large for shared memory (dim %d)", what, a.dim);
+  const cuuint64_t row_bytes = static_cast<cuuint64_t>(a.dim) * 2;
+  const cuuint64_t qdims[3] = {static_cast<cuuint64_t>(a.dim), static_cast<cuuint64_t>(a.rows), static_cast<cuuint64_t>(a.seqs)};
+  const cuuint64_t qstr[2] = {row_bytes, row_bytes * a.rows};
+  const cuuint32_t qbox[3] = {64, static_cast<cuuint32_t>(a.N), 1};
+  li_status s = encode_map(c, &a.map_q, LI_BF16, 3, const_cast<void*>(q), qdims, qstr, qbox, 128);
+  if (s != LI_OK) return s;
+  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(a.dim), static_cast<cuuint64_t>(a.pool_rows)};
+  const cuuint64_t str[1] = {row_bytes};
+  const cuuint32_t one[2] = {64, 1}, box[2] = {64, static_cast<cuuint32_t>(a.box)};
+  if ((s = encode_map(c, &a.map_rows, LI_BF16, 2, cache->data, dims, str, one, 128, false)) != LI_OK) return s;
+  if (a.box && !sel && (s = encode_map(c, &a.map_box, LI_BF16, 2, cache->data, dims, str, box, 128)) != LI_OK) return s;
+  if (sel) a.box = 0;
+  (void)cudaGetLastError();
+  {
+    Launch L(c, st, "latent_attn", a.grid, 416, static_cast<int>(a.smem_bytes));
+    const cudaError_t e = launch_latent_mma(a, st);
+    L.done();
+    if (e != cudaSuccess) return cuda_fail(c, e, "latent attention launch");
+  }
+  if (a.grid == 1) return LI_OK;
+  Launch L(c, st, "latent_join", a.grid - 1, 128, 0);
+  const cudaError_t e = launch_latent_join(a, st);
+  L.done();
+  return e == cudaSuccess ? LI_OK : cuda_fail(c, e, "latent attention join launch");
+}
+
 li_status latent_attention(li_ctx* c, const li_paged_cache* cache, const void* q, int T, int H, int d_v, float scale,
                            const int32_t* q_pos, const int32_t* sel, int k, void* out, float* lse, void* ws,
                            size_t ws_bytes, cudaStream_t st) {
@@ -202,6 +262,8 @@ li_status latent_attention(li_ctx* c, const li_paged_cache* cache, const void* q
     return fail(c, LI_ERR_ALIGN, "%s: q must be 16-byte aligned, the other tensors to their elements", what);
   if ((s = check_attn_ws(c, ws, ws_bytes, li_attention_workspace_bytes(c, H, d_v), what)) != LI_OK) return s;
   if ((s = check_device(c, what)) != LI_OK) return s;
+  if (cache->dtype == LI_BF16)
+    return latent_mma(c, cache, q, T, H, d_v, scale, q_pos, sel, k, out, lse, ws, st);
   LatentAttnArgs a;
   memset(&a, 0, sizeof(a));
   a.q = q;
@@ -271,8 +333,8 @@ li_status prompt_attention(li_ctx* c, const li_prompt* p, void* out, float* lse,
 extern "C" {
 
 size_t li_attention_workspace_bytes(const li_ctx* c, int H, int d_v) {
-  if (!c || H < 1 || d_v < 1) return 0;
-  return kAttnHeader;
+  if (!c || H < 1 || d_v < 1 || d_v > 512) return 0;
+  return kAttnHeader + latent_part_bytes(c->num_sms, d_v);
 }
 
 li_status li_norm_rope(li_ctx* c, const li_head_rows* sets, int n_sets, li_dtype dtype, int64_t n_tok, const int32_t* pos,

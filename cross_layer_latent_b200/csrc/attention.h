@@ -57,6 +57,44 @@ struct LatentAttnArgs {
   float scale;
 };
 
+// bf16 on the tensor cores (latent_mma.cu).
+struct alignas(64) LatentMmaArgs {
+  CUtensorMap map_q;      // queries: dims {dim, rows, seqs}, box {64, N, 1}
+  CUtensorMap map_rows;   // pool rows one by one: dims {dim, pool_rows}, box {64, 1} (gathers of four)
+  CUtensorMap map_box;    // pool rows of a page: box {64, box}
+  const int32_t* page_table;
+  const int32_t* lengths;
+  const int32_t* q_pos;
+  const int32_t* sel;
+  void* out;
+  float* lse;
+  float* part_o;          // [2 grid][64][part_stride] sums of the parts, and
+  float* part_ml;         // [2 grid][64][2] their maxima (log2) and weight sums
+  int* status;
+  uint64_t wait_ns;
+  float scale_log2;       // scale * log2(e)
+  int seqs;               // work units with rows of their own: sequences, with sel (sequence, query) pairs
+  int rows;               // query rows of a unit: T * H, with sel H
+  int T, H, k, dim, d_v;
+  int n_pages, page_size, max_pages, pool_rows;
+  int box;                // rows of a box (a divisor of the page size), 0: gather always
+  // filled by latent_mma_layout
+  int N, groups;          // MMA columns, groups of N rows in a unit
+  int nb, last_ksteps;    // 64-column blocks of a row, 16-element K steps of the last one
+  int m_blocks;           // blocks of 128 values
+  int slots, bufs;        // 16 KB slots of a tile, tiles held in shared memory
+  int s_bufs;             // score buffers in tensor memory
+  int part_stride;
+  int grid;
+  uint32_t tmem_cols, smem_bytes;
+};
+
+constexpr int latent_part_stride(int d_v) { return (d_v + 3) / 4 * 4; }
+size_t latent_part_bytes(int num_sms, int d_v);
+bool latent_mma_layout(LatentMmaArgs* a, int num_sms, int max_smem);
+cudaError_t launch_latent_mma(const LatentMmaArgs& a, cudaStream_t st);
+cudaError_t launch_latent_join(const LatentMmaArgs& a, cudaStream_t st);
+
 cudaError_t launch_latent_attn_rows(const LatentAttnArgs& a, li_dtype dtype, cudaStream_t st);
 cudaError_t launch_prompt_attn_rows(const li_prompt& p, void* out, float* lse, cudaStream_t st);
 
