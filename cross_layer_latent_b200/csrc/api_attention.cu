@@ -292,6 +292,64 @@ li_status latent_attention(li_ctx* c, const li_paged_cache* cache, const void* q
   return e == cudaSuccess ? LI_OK : cuda_fail(c, e, "latent attention launch");
 }
 
+// A tensor of rows [tokens][heads][d] as a map with 128-row boxes of 64
+// columns (heads = 0: no head dimension).  Strides of dimensions of one
+// element are free, so they are set to something the map takes.
+li_status rows_map(li_ctx* c, CUtensorMap* m, const void* base, int d, int heads, int tokens, int64_t head_stride,
+                   int64_t tok_stride) {
+  const cuuint64_t hs = static_cast<cuuint64_t>(heads > 1 ? head_stride : (d + 7) / 8 * 8) * 2;
+  const cuuint64_t ts = static_cast<cuuint64_t>(tokens > 1 ? tok_stride : (d + 7) / 8 * 8) * 2;
+  if (heads == 0) {
+    const cuuint64_t dims[2] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(tokens)}, str[1] = {ts};
+    const cuuint32_t box[2] = {64, 128};
+    return encode_map(c, m, LI_BF16, 2, const_cast<void*>(base), dims, str, box, 128);
+  }
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(heads), static_cast<cuuint64_t>(tokens)};
+  const cuuint64_t str[2] = {hs, ts};
+  const cuuint32_t box[3] = {64, 1, 128};
+  return encode_map(c, m, LI_BF16, 3, const_cast<void*>(base), dims, str, box, 128);
+}
+
+li_status prompt_mma(li_ctx* c, const li_prompt& p, void* out, float* lse, void* ws, cudaStream_t st) {
+  const char* what = "li_prompt_attention";
+  PromptMmaArgs a;
+  memset(&a, 0, sizeof(a));
+  a.cu_q = p.cu_q;
+  a.cu_k = p.cu_k;
+  a.out = out;
+  a.lse = lse;
+  a.status = at<int>(ws, 0);
+  a.next_unit = at<unsigned int>(ws, 128);
+  a.done = at<unsigned int>(ws, 132);
+  a.wait_ns = c->wait_ns;
+  // a scale of 0 makes every weight equal; the smallest steps of the scores do the same and keep -inf apart
+  a.scale_log2 = std::max(std::fabs(p.scale) * 1.44269504089f, 1e-30f);
+  a.negate = p.scale < 0.f;
+  a.causal = p.causal != 0;
+  a.batch = p.batch;
+  a.H = p.H;
+  a.total_q = p.total_q;
+  a.total_k = p.total_k;
+  a.max_q = p.max_q;
+  a.d_nope = p.d_nope;
+  a.d_rope = p.d_rope;
+  a.d_v = p.d_v;
+  if (!prompt_mma_layout(&a, c->num_sms, c->max_smem_optin))
+    return fail(c, LI_ERR_UNSUPPORTED, "%s: operands too large for shared memory", what);
+  li_status s = rows_map(c, &a.map_q, p.q, p.d_nope + p.d_rope, p.H, p.total_q, p.q_head_stride, p.q_tok_stride);
+  if (s == LI_OK && p.total_k > 0) {
+    s = rows_map(c, &a.map_k, p.k_nope, p.d_nope, p.H, p.total_k, p.k_head_stride, p.k_tok_stride);
+    if (s == LI_OK) s = rows_map(c, &a.map_v, p.v, p.d_v, p.H, p.total_k, p.v_head_stride, p.v_tok_stride);
+    if (s == LI_OK && p.d_rope) s = rows_map(c, &a.map_kr, p.k_rope, p.d_rope, 0, p.total_k, 0, p.kr_tok_stride);
+  }
+  if (s != LI_OK) return s;
+  (void)cudaGetLastError();
+  Launch L(c, st, "prompt_attn", a.grid, 352, static_cast<int>(a.smem_bytes));
+  const cudaError_t e = launch_prompt_mma(a, st);
+  L.done();
+  return e == cudaSuccess ? LI_OK : cuda_fail(c, e, "prompt attention launch");
+}
+
 li_status prompt_attention(li_ctx* c, const li_prompt* p, void* out, float* lse, void* ws, size_t ws_bytes, cudaStream_t st) {
   const char* what = "li_prompt_attention";
   if (!p) return fail(c, LI_ERR_ARG, "%s: the argument record is NULL", what);
@@ -316,11 +374,16 @@ li_status prompt_attention(li_ctx* c, const li_prompt* p, void* out, float* lse,
       p->q_tok_stride % m || p->q_head_stride % m || p->k_tok_stride % m || p->k_head_stride % m || p->kr_tok_stride % m ||
       p->v_tok_stride % m || p->v_head_stride % m)
     return fail(c, LI_ERR_ALIGN, "%s: every row must be 16-byte aligned", what);
+  if ((p->H > 1 && (p->q_head_stride <= 0 || p->k_head_stride <= 0 || p->v_head_stride <= 0)) ||
+      (p->total_q > 1 && p->q_tok_stride <= 0) ||
+      (p->total_k > 1 && (p->k_tok_stride <= 0 || p->v_tok_stride <= 0 || (p->d_rope && p->kr_tok_stride <= 0))))
+    return fail(c, LI_ERR_ARG, "%s: strides must be positive", what);
   if ((s = check_attn_ws(c, ws, ws_bytes, li_attention_workspace_bytes(c, p->H, p->d_v), what)) != LI_OK) return s;
   if ((s = check_device(c, what)) != LI_OK) return s;
   if (p->total_q == 0 || p->max_q == 0) return LI_OK;
   li_prompt a = *p;
   a.max_q = std::min(p->max_q, p->total_q);
+  if (p->dtype == LI_BF16) return prompt_mma(c, a, out, lse, ws, st);
   (void)cudaGetLastError();
   Launch L(c, st, "prompt_attn_rows", 0, 256, 0);
   const cudaError_t e = launch_prompt_attn_rows(a, out, lse, st);

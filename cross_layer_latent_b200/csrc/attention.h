@@ -95,6 +95,35 @@ bool latent_mma_layout(LatentMmaArgs* a, int num_sms, int max_smem);
 cudaError_t launch_latent_mma(const LatentMmaArgs& a, cudaStream_t st);
 cudaError_t launch_latent_join(const LatentMmaArgs& a, cudaStream_t st);
 
+struct alignas(64) PromptMmaArgs {
+  CUtensorMap map_q;      // dims {d_nope + d_rope, H, total_q}, box {64, 1, 128}
+  CUtensorMap map_k;      // dims {d_nope, H, total_k}, box {64, 1, 128}
+  CUtensorMap map_kr;     // dims {d_rope, total_k}, box {64, 128}
+  CUtensorMap map_v;      // dims {d_v, H, total_k}, box {64, 1, 128}
+  const int32_t* cu_q;
+  const int32_t* cu_k;
+  void* out;
+  float* lse;
+  unsigned int* next_unit;  // workspace counters, zero between calls
+  unsigned int* done;
+  int* status;
+  uint64_t wait_ns;
+  float scale_log2;       // |scale| * log2(e)
+  int negate;             // scale < 0
+  int causal;
+  int batch, H, total_q, total_k, max_q;
+  int d_nope, d_rope, d_v;
+  // filled by prompt_mma_layout
+  int nope_blocks, rope_blocks, v_blocks;   // 64-column blocks
+  int nope_ksteps, rope_ksteps;             // 16-element K steps of each part's last block
+  int ring;                                 // 16 KB blocks of the ring
+  int grid;
+  uint32_t smem_bytes;
+};
+
+bool prompt_mma_layout(PromptMmaArgs* a, int num_sms, int max_smem);
+cudaError_t launch_prompt_mma(const PromptMmaArgs& a, cudaStream_t st);
+
 cudaError_t launch_latent_attn_rows(const LatentAttnArgs& a, li_dtype dtype, cudaStream_t st);
 cudaError_t launch_prompt_attn_rows(const li_prompt& p, void* out, float* lse, cudaStream_t st);
 

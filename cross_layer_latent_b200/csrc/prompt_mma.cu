@@ -1,0 +1,512 @@
+// prompt_mma.cu -- latent attention in expanded form on the tensor cores:
+// causal (or full) attention of ragged prompts, head by head.
+//
+// A unit of work is 256 queries of one head, as two tiles of 128, and a walk
+// over the keys in tiles of 128:
+//     S_q = Q_q K^T      [128 x 128]   A = Q, B = K (both K-major in shared memory)
+//     P_q = exp2(S_q - m)              one query row a thread
+//     O_q += P_q V       [128 x d_v]   A = P from tensor memory, B = V (MN-major)
+// The two tiles alternate: while one's scores are turned into weights, the
+// other's products run, so the tensor cores wait for neither.  At d_nope +
+// d_rope = 192, d_v = 128 a tile pair costs 2560 cycles of MMA (12 steps of 64
+// and 8 of 64 for each tile) against 2048 cycles of special-function unit (128
+// x 128 exponentials a tile at 16 a cycle): the MMAs bound it.
+// Tensor memory is full: S0, S1 (P takes the place of S), O0, O1.  Shared
+// memory holds both query tiles (96 KB) and a ring of 16 KB blocks, 128
+// tokens x 64 columns of K (k_nope of the head, then the k_rope that all heads
+// share) or of V; blocks are freed one by one.
+//
+// The running maximum moves only when a row exceeds it by more than 8 (in
+// powers of two): weights stay below 256, which costs their bf16 rounding
+// (relative) and the fp32 sums nothing, and the outputs are seldom rescaled.
+// The sums are taken before the weights are rounded.
+//
+// CTAs are persistent and take the next unit from a counter; units of a
+// group of heads whose keys and values fit the L2 together come longest first.
+#include <algorithm>
+
+#include "attention.h"
+#include "attn_sm100.cuh"
+#include "internal.h"
+
+namespace li {
+
+namespace {
+
+constexpr int kTile = 128;
+constexpr int kRows = 2 * kTile;                 // queries of a unit
+constexpr int kBlockBytes = kTile * 128;
+constexpr int kSoftWarps = 8;                    // a warpgroup for each query tile
+constexpr int kMmaWarp = 8, kLoadWarp = 9;   // and one that zeroes
+constexpr int kThreads = 32 * 11;
+constexpr int kMaxRing = 13;
+constexpr float kGrow = 8.f;
+constexpr float kNoMax = -1e30f;
+constexpr uint64_t kDrainNs = 1000ull * 1000ull;
+constexpr int64_t kL2Share = int64_t(48) << 20;  // keys and values of the heads that run together
+
+struct Unit {
+  int q0, nq, k0, nk;    // rows of the sequence in q and k
+  int row0, h;           // first query of the unit; h < 0: no more units
+};
+
+struct Smem {
+  uint64_t full[kMaxRing], empty[kMaxRing], raw[kMaxRing];
+  uint64_t unit_full[2], unit_empty[2];
+  uint64_t q_full, q_empty, s_full[2], p_full[2], o_full[2], o_empty[2], drain;
+  Unit unit[2];
+  uint32_t tmem;
+  int abort_flag;
+};
+
+// Keys that query i of the sequence sees.
+__device__ __forceinline__ int key_limit(const PromptMmaArgs& a, const Unit& u, int i) {
+  if (!a.causal) return u.nk;
+  const int64_t n = static_cast<int64_t>(i) + 1 + u.nk - u.nq;
+  return static_cast<int>(max(min(n, static_cast<int64_t>(u.nk)), int64_t(0)));
+}
+// Key tiles of query tile q (0 or 1) of the unit: those that its last row sees.
+__device__ __forceinline__ int key_tiles(const PromptMmaArgs& a, const Unit& u, int q) {
+  const int first = u.row0 + q * kTile;
+  if (first >= u.nq) return 0;
+  return (key_limit(a, u, min(first + kTile, u.nq) - 1) + kTile - 1) / kTile;
+}
+
+__device__ __forceinline__ int seq_rows(const int32_t* cu, int b, int total, int* first) {
+  const int x = min(max(cu[b], 0), total);
+  *first = x;
+  return min(max(cu[b + 1], x), total) - x;
+}
+__device__ __forceinline__ int seq_queries(const PromptMmaArgs& a, int b, int* first) {
+  return min(seq_rows(a.cu_q, b, a.total_q, first), a.max_q);
+}
+__device__ __forceinline__ int seq_units(const PromptMmaArgs& a, int b) {
+  int f;
+  return (seq_queries(a, b, &f) + kRows - 1) / kRows;
+}
+
+// Unit number x of all (the whole warp calls it).
+__device__ __forceinline__ Unit find_unit(const PromptMmaArgs& a, int64_t x, int64_t total, int lane) {
+  Unit u;
+  u.h = -1;
+  if (x >= total) return u;
+  int b = a.batch - 1;
+  for (int b0 = 0; b0 < a.batch; b0 += 32) {
+    const int64_t c = b0 + lane < a.batch ? static_cast<int64_t>(seq_units(a, b0 + lane)) * a.H : 0;
+    int64_t end = c;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t v = __shfl_up_sync(0xffffffffu, end, o);
+      if (lane >= o) end += v;
+    }
+    const int past = __popc(__ballot_sync(0xffffffffu, b0 + lane < a.batch && end <= x));
+    if (past < min(32, a.batch - b0)) {
+      b = b0 + past;
+      x -= __shfl_sync(0xffffffffu, end - c, past);
+      break;
+    }
+    x -= __shfl_sync(0xffffffffu, end, 31);
+  }
+  int f;
+  u.nq = seq_queries(a, b, &u.q0);
+  (void)f;
+  u.nk = seq_rows(a.cu_k, b, a.total_k, &u.k0);
+  // causal limits go by the whole sequence, also where max_q cuts it
+  int whole = seq_rows(a.cu_q, b, a.total_q, &f);
+  if (a.causal && whole > u.nq) u.nk = max(u.nk - (whole - u.nq), 0);
+  const int tiles = (u.nq + kRows - 1) / kRows;
+  const int64_t per_head = static_cast<int64_t>(max(u.nk, 1)) * (a.d_nope + a.d_v) * 2;
+  const int hg = static_cast<int>(max(min(kL2Share / per_head, static_cast<int64_t>(a.H)), int64_t(1)));
+  const int64_t per_group = static_cast<int64_t>(hg) * tiles;
+  const int g = static_cast<int>(x / per_group);
+  const int r = static_cast<int>(x - g * per_group);
+  const int heads = min(hg, a.H - g * hg);
+  u.h = g * hg + r % heads;
+  u.row0 = (tiles - 1 - r / heads) * kRows;
+  return u;
+}
+
+__global__ void __launch_bounds__(kThreads, 1) prompt_mma_kernel(const __grid_constant__ PromptMmaArgs a) {
+  extern __shared__ uint8_t raw_smem[];
+  uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw_smem) + 1023) & ~uintptr_t(1023));
+  const int nkb = a.nope_blocks + a.rope_blocks;
+  uint8_t* ring = base + 2 * nkb * kBlockBytes;
+  Smem& sm = *reinterpret_cast<Smem*>(ring + a.ring * kBlockBytes);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const WaitCtl wc{&sm.abort_flag, a.status, a.wait_ns};
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < a.ring; ++i) {
+      mbar_init(&sm.full[i], 1);
+      mbar_init(&sm.empty[i], 1);
+      mbar_init(&sm.raw[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&sm.unit_full[i], 1);
+      mbar_init(&sm.unit_empty[i], kSoftWarps + 2);
+      mbar_init(&sm.s_full[i], 1);
+      mbar_init(&sm.p_full[i], 4);
+      mbar_init(&sm.o_full[i], 1);
+      mbar_init(&sm.o_empty[i], 4);
+    }
+    mbar_init(&sm.q_full, 1);
+    mbar_init(&sm.q_empty, 1);
+    mbar_init(&sm.drain, 1);
+    sm.abort_flag = 0;
+    fence_barrier_init();
+    tma_prefetch_desc(&a.map_q);
+    if (a.total_k > 0) {
+      tma_prefetch_desc(&a.map_k);
+      tma_prefetch_desc(&a.map_v);
+    }
+  }
+  if (warp == kMmaWarp) {
+    tmem_alloc(&sm.tmem, 512);
+    tmem_relinquish();
+  }
+  pdl_begin();
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = sm.tmem;
+
+  if (warp < kSoftWarps) {
+    // ------------------------------------------------ softmax and output of query tile q
+    const int q = warp >> 2, quad = warp & 3;
+    const uint32_t lanes = static_cast<uint32_t>(quad * 32) << 16;
+    const uint32_t s_tm = tmem + q * 128 + lanes, o_tm = tmem + 256 + q * 128 + lanes;
+    const int r = quad * 32 + lane;
+    int64_t tile = 0, outs = 0;
+    bool ok = true;
+    for (int64_t un = 0; ok; ++un) {
+      ok = __all_sync(0xffffffffu, bounded_wait_sleep(&sm.unit_full[un & 1], static_cast<uint32_t>(un >> 1) & 1u, wc));
+      if (!ok) break;
+      const Unit u = sm.unit[un & 1];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm.unit_empty[un & 1]);
+      if (u.h < 0) break;
+      const int first = u.row0 + q * kTile;
+      const int n = key_tiles(a, u, q);
+      const int i = first + r;
+      const int lim = i < u.nq ? key_limit(a, u, i) : u.nk;
+      float m = kNoMax, l = 0.f;
+      for (int t = 0; t < n; ++t, ++tile) {
+        ok = __all_sync(0xffffffffu, bounded_wait(&sm.s_full[q], static_cast<uint32_t>(tile) & 1u, wc));
+        if (!ok) break;
+        tc_fence_after();
+        float x[128];
+        {
+          uint32_t xr[4][32];
+#pragma unroll
+          for (int c = 0; c < 4; ++c) tmem_ld<32>(s_tm + 32 * c, xr[c]);
+          tmem_wait_ld();
+#pragma unroll
+          for (int c = 0; c < 128; ++c) x[c] = __uint_as_float(xr[c / 32][c % 32]);
+        }
+        if (a.negate) {
+#pragma unroll
+          for (int c = 0; c < 128; ++c) x[c] = -x[c];
+        }
+        if (__any_sync(0xffffffffu, (t + 1) * kTile > lim)) {
+          const int left = lim - t * kTile;
+#pragma unroll
+          for (int c = 0; c < 128; ++c)
+            if (c >= left) x[c] = -INFINITY;
+        }
+        float top = x[0];
+#pragma unroll
+        for (int c = 1; c < 127; c += 2) top = fmaxf(fmaxf(top, x[c]), x[c + 1]);
+        top = fmaxf(top, x[127]);
+        const bool grow = (top - m) * a.scale_log2 > kGrow;
+        if (__any_sync(0xffffffffu, grow)) {
+          const float now = grow ? top : m;
+          const float keep = exp2_fast((m - now) * a.scale_log2);
+          m = now;
+          l *= keep;
+          if (t > 0) {
+            // the previous tile's product is complete: s_full was committed after it
+#pragma unroll 1
+            for (int c = 0; c < a.v_blocks * 64; c += 16) {
+              uint32_t o[16];
+              tmem_ld<16>(o_tm + c, o);
+              tmem_wait_ld();
+#pragma unroll
+              for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * keep);
+              tmem_st<16>(o_tm + c, o);
+            }
+          }
+        }
+        const float ms = m * a.scale_log2;
+        float s0 = 0.f, s1 = 0.f;
+#pragma unroll
+        for (int c = 0; c < 128; c += 32) {
+          uint32_t pk[16];
+#pragma unroll
+          for (int e = 0; e < 32; e += 2) {
+            const float p0 = exp2_fast(fmaf(x[c + e], a.scale_log2, -ms));
+            const float p1 = exp2_fast(fmaf(x[c + e + 1], a.scale_log2, -ms));
+            s0 += p0;
+            s1 += p1;
+            pk[e / 2] = pack_bf16(p0, p1);
+          }
+          tmem_st<16>(s_tm + c / 2, pk);
+        }
+        l += s0 + s1;
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.p_full[q]);
+      }
+      if (!ok) break;
+      if (first >= u.nq) continue;
+      if (n > 0) {
+        ok = __all_sync(0xffffffffu, bounded_wait(&sm.o_full[q], static_cast<uint32_t>(outs) & 1u, wc));
+        if (!ok) break;
+        ++outs;
+        tc_fence_after();
+      }
+      const float inv = l > 0.f ? 1.f / l : 0.f;
+      const int64_t row = static_cast<int64_t>(u.q0 + i) * a.H + u.h;
+      for (int c = 0; c < a.d_v; c += 32) {
+        uint32_t o[32];
+        if (n > 0) {
+          tmem_ld<32>(o_tm + c, o);
+          tmem_wait_ld();
+        } else {
+#pragma unroll
+          for (int e = 0; e < 32; ++e) o[e] = 0u;
+        }
+        if (i < u.nq) {
+          uint4* out = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + row * a.d_v + c);
+#pragma unroll
+          for (int e = 0; e < 32; e += 8) {
+            if (c + e < a.d_v) {
+              uint4 w;
+              w.x = pack_bf16(__uint_as_float(o[e]) * inv, __uint_as_float(o[e + 1]) * inv);
+              w.y = pack_bf16(__uint_as_float(o[e + 2]) * inv, __uint_as_float(o[e + 3]) * inv);
+              w.z = pack_bf16(__uint_as_float(o[e + 4]) * inv, __uint_as_float(o[e + 5]) * inv);
+              w.w = pack_bf16(__uint_as_float(o[e + 6]) * inv, __uint_as_float(o[e + 7]) * inv);
+              out[e / 8] = w;
+            }
+          }
+        }
+      }
+      if (a.lse && i < u.nq) a.lse[row] = l > 0.f ? (m * a.scale_log2 + log2f(l)) * 0.69314718056f : -INFINITY;
+      if (n > 0) {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.o_empty[q]);
+      }
+    }
+  } else if (warp == kMmaWarp) {
+    // ------------------------------------------------ MMA issue, one lane
+    if (elect_one()) {
+      const uint32_t id_s = make_instr_desc(1, 128, 128);
+      const uint32_t id_o = make_instr_desc(1, 128, 64) | kMajorMnB;
+      const uint32_t q_smem = smem_addr(base), ring_smem = smem_addr(ring);
+      int64_t blocks = 0;                        // ring position of the unit's first block
+      int64_t ptile[2] = {0, 0}, outs[2] = {0, 0};
+      bool ok = true;
+      auto slot_of = [&](int64_t i, uint32_t* ph) {
+        *ph = static_cast<uint32_t>(i / a.ring) & 1u;
+        return static_cast<int>(i % a.ring);
+      };
+      const int per = nkb + a.v_blocks;
+      for (int64_t un = 0, busy = 0; ok; ++un) {
+        if (!(ok = bounded_wait(&sm.unit_full[un & 1], static_cast<uint32_t>(un >> 1) & 1u, wc))) break;
+        const Unit u = sm.unit[un & 1];
+        mbar_arrive(&sm.unit_empty[un & 1]);
+        if (u.h < 0) break;
+        const int n[2] = {key_tiles(a, u, 0), key_tiles(a, u, 1)};
+        const int nt = max(n[0], n[1]);
+        if (nt == 0) continue;
+        if (!(ok = bounded_wait(&sm.q_full, static_cast<uint32_t>(busy) & 1u, wc))) break;
+        ++busy;
+        auto scores = [&](int q, int t, bool last) {
+          for (int j = 0; j < nkb; ++j) {
+            uint32_t ph;
+            const int s = slot_of(blocks + static_cast<int64_t>(t) * per + j, &ph);
+            if (!bounded_wait(&sm.full[s], ph, wc)) return false;
+            tc_fence_after();
+            const uint64_t da = desc_sw128(q_smem + (q * nkb + j) * kBlockBytes, 16, 1024);
+            const uint64_t db = desc_sw128(ring_smem + s * kBlockBytes, 16, 1024);
+            const int ks = j == a.nope_blocks - 1 ? a.nope_ksteps : (j == nkb - 1 ? a.rope_ksteps : 4);
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)
+              if (kk < ks) umma<kKindBF16>(tmem + q * 128, da + 2 * kk, db + 2 * kk, id_s, (j > 0 || kk > 0) ? 1u : 0u);
+            if (last) umma_commit(&sm.empty[s]);
+          }
+          umma_commit(&sm.s_full[q]);
+          return true;
+        };
+        auto values = [&](int q, int t, bool last) {
+          if (t == 0 && outs[q] > 0 && !bounded_wait(&sm.o_empty[q], static_cast<uint32_t>(outs[q] - 1) & 1u, wc)) return false;
+          if (!bounded_wait(&sm.p_full[q], static_cast<uint32_t>(ptile[q]) & 1u, wc)) return false;
+          ++ptile[q];
+          tc_fence_after();
+          for (int j = 0; j < a.v_blocks; ++j) {
+            uint32_t ph;
+            const int s = slot_of(blocks + static_cast<int64_t>(t) * per + nkb + j, &ph);
+            if (!bounded_wait(&sm.full[s], ph, wc)) return false;
+            tc_fence_after();
+            const uint64_t dv = desc_sw128(ring_smem + s * kBlockBytes, 16, 1024);
+#pragma unroll
+            for (int kk = 0; kk < 8; ++kk)
+              umma_ts_bf16(tmem + 256 + q * 128 + j * 64, tmem + q * 128 + kk * 8, dv + kk * 128, id_o, (t > 0 || kk > 0) ? 1u : 0u);
+            if (last) umma_commit(&sm.empty[s]);
+          }
+          if (t == n[q] - 1) {
+            umma_commit(&sm.o_full[q]);
+            ++outs[q];
+          }
+          return true;
+        };
+        // a block is free after the last of the two tiles that use it
+        for (int q = 0; q < 2 && ok; ++q)
+          if (n[q] > 0) ok = scores(q, 0, q == 1 || n[1] == 0);
+        if (ok && nt == 1) umma_commit(&sm.q_empty);
+        for (int t = 0; t < nt && ok; ++t) {
+          for (int q = 0; q < 2 && ok; ++q) {
+            if (t < n[q]) ok = values(q, t, q == 1 || t >= n[1]);
+            if (ok && t + 1 < n[q]) ok = scores(q, t + 1, q == 1 || t + 1 >= n[1]);
+          }
+          if (ok && t + 2 == nt) umma_commit(&sm.q_empty);
+        }
+        blocks += static_cast<int64_t>(nt) * per;
+      }
+      umma_commit(&sm.drain);
+      drain_wait(&sm.drain, 0, kDrainNs);
+    }
+    __syncwarp();
+  } else if (warp == kLoadWarp) {
+    // ------------------------------------------------ units and loads
+    int64_t units = 0;
+    for (int b = lane; b < a.batch; b += 32) units += seq_units(a, b);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) units += __shfl_xor_sync(0xffffffffu, units, o);
+    const int64_t total = units * a.H;
+    int64_t next = blockIdx.x, blk = 0, queries = 0;
+    bool ok = true;
+    for (int64_t un = 0, busy = 0; ok; ++un) {
+      const Unit u = find_unit(a, next, total, lane);
+      if (u.h >= 0 && lane == 0) next = static_cast<int64_t>(gridDim.x) + atomicAdd(a.next_unit, 1u);
+      next = __shfl_sync(0xffffffffu, next, 0);
+      if (un >= 2) ok = __all_sync(0xffffffffu, bounded_wait(&sm.unit_empty[un & 1], static_cast<uint32_t>((un >> 1) - 1) & 1u, wc));
+      if (!ok) break;
+      if (lane == 0) {
+        sm.unit[un & 1] = u;
+        mbar_arrive(&sm.unit_full[un & 1]);
+      }
+      if (u.h < 0) break;
+      const int n0 = key_tiles(a, u, 0), n1 = key_tiles(a, u, 1), nt = max(n0, n1);
+      if (nt == 0) continue;
+      int good = 1;
+      if (lane == 0) {
+        if (busy > 0) good = bounded_wait(&sm.q_empty, static_cast<uint32_t>(busy - 1) & 1u, wc);
+        if (good) {
+          const int tiles = n1 > 0 ? 2 : 1;
+          mbar_arrive_expect_tx(&sm.q_full, tiles * nkb * kBlockBytes);
+          ++queries;
+          for (int q = 0; q < tiles; ++q)
+            for (int j = 0; j < nkb; ++j)
+              tma_load_3d(base + (q * nkb + j) * kBlockBytes, &a.map_q, &sm.q_full,
+                          j < a.nope_blocks ? 64 * j : a.d_nope + 64 * (j - a.nope_blocks), u.h, u.q0 + u.row0 + q * kTile);
+          for (int t = 0; t < nt && good; ++t) {
+            const int row = u.k0 + t * kTile;
+            for (int j = 0; j < nkb + a.v_blocks && good; ++j, ++blk) {
+              const int s = static_cast<int>(blk % a.ring);
+              const int64_t use = blk / a.ring;
+              if (use > 0) good = bounded_wait(&sm.empty[s], static_cast<uint32_t>(use - 1) & 1u, wc);
+              if (!good) break;
+              uint8_t* dst = ring + s * kBlockBytes;
+              // values past the sequence's end are zeroed before anyone reads them
+              uint64_t* bar = j >= nkb && (t + 1) * kTile > u.nk ? &sm.raw[s] : &sm.full[s];
+              mbar_arrive_expect_tx(bar, kBlockBytes);
+              if (j < a.nope_blocks) tma_load_3d(dst, &a.map_k, bar, 64 * j, u.h, row);
+              else if (j < nkb) tma_load_2d(dst, &a.map_kr, bar, 64 * (j - a.nope_blocks), row);
+              else tma_load_3d(dst, &a.map_v, bar, 64 * (j - nkb), u.h, row);
+            }
+          }
+        }
+      }
+      ok = __shfl_sync(0xffffffffu, good, 0) != 0;
+      ++busy;
+    }
+    if (lane == 0) {
+      // the copies in flight land before the CTA ends, whichever role gave up
+      for (int64_t f = max(blk - a.ring, int64_t(0)); f < blk; ++f)
+        drain_wait(&sm.full[f % a.ring], static_cast<uint32_t>(f / a.ring) & 1u, kDrainNs);
+      if (queries > 0) drain_wait(&sm.q_full, static_cast<uint32_t>(queries - 1) & 1u, kDrainNs);
+    }
+    __syncwarp();
+  } else {
+    // ------------------------------------------------ zeroes behind a sequence's last values
+    int64_t blocks = 0;
+    uint32_t raw_phase = 0;
+    bool ok = true;
+    for (int64_t un = 0; ok; ++un) {
+      ok = __all_sync(0xffffffffu, bounded_wait_sleep(&sm.unit_full[un & 1], static_cast<uint32_t>(un >> 1) & 1u, wc));
+      if (!ok) break;
+      const Unit u = sm.unit[un & 1];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm.unit_empty[un & 1]);
+      if (u.h < 0) break;
+      const int nt = max(key_tiles(a, u, 0), key_tiles(a, u, 1));
+      const int per = nkb + a.v_blocks;
+      if (nt > 0 && nt * kTile > u.nk) {
+        const int keep = u.nk - (nt - 1) * kTile;
+        for (int j = 0; j < a.v_blocks && ok; ++j) {
+          const int s = static_cast<int>((blocks + static_cast<int64_t>(nt - 1) * per + nkb + j) % a.ring);
+          ok = __all_sync(0xffffffffu, bounded_wait_sleep(&sm.raw[s], (raw_phase >> s) & 1u, wc));
+          if (!ok) break;
+          raw_phase ^= 1u << s;
+          uint4* rows = reinterpret_cast<uint4*>(ring + s * kBlockBytes);
+          for (int x = keep * 8 + lane; x < kTile * 8; x += 32) rows[x] = make_uint4(0u, 0u, 0u, 0u);
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sm.full[s]);
+        }
+      }
+      blocks += static_cast<int64_t>(nt) * per;
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == kMmaWarp) tmem_dealloc(tmem, 512);
+  // the last CTA leaves the counters as it found them
+  if (threadIdx.x == 0) {
+    unsigned prev;
+    asm volatile("atom.acq_rel.gpu.global.add.u32 %0, [%1], 1;" : "=r"(prev) : "l"(a.done) : "memory");
+    if (prev == gridDim.x - 1) {
+      *a.next_unit = 0u;
+      *a.done = 0u;
+    }
+  }
+}
+
+}  // namespace
+
+bool prompt_mma_layout(PromptMmaArgs* a, int num_sms, int max_smem) {
+  a->nope_blocks = (a->d_nope + 63) / 64;
+  a->rope_blocks = (a->d_rope + 63) / 64;
+  a->v_blocks = (a->d_v + 63) / 64;
+  a->nope_ksteps = (a->d_nope - 64 * (a->nope_blocks - 1) + 15) / 16;
+  a->rope_ksteps = (a->d_rope + 15) / 16;
+  const int64_t q = 2ll * (a->nope_blocks + a->rope_blocks) * kBlockBytes;
+  const int64_t room = static_cast<int64_t>(max_smem) - 1024 - q - static_cast<int64_t>(sizeof(Smem));
+  a->ring = static_cast<int>(std::min<int64_t>(kMaxRing, room / kBlockBytes));
+  if (a->ring < a->nope_blocks + a->rope_blocks + a->v_blocks) return false;
+  a->smem_bytes = static_cast<uint32_t>(1024 + q + a->ring * kBlockBytes + sizeof(Smem));
+  const int64_t units = (static_cast<int64_t>(a->total_q) / kRows + a->batch) * a->H;
+  a->grid = static_cast<int>(std::min<int64_t>(num_sms, units));
+  return true;
+}
+
+cudaError_t launch_prompt_mma(const PromptMmaArgs& a, cudaStream_t st) {
+  const cudaError_t e = raise_smem_limit(reinterpret_cast<const void*>(prompt_mma_kernel), static_cast<int>(a.smem_bytes));
+  if (e != cudaSuccess) return e;
+  return launch_pdl(prompt_mma_kernel, dim3(a.grid), dim3(kThreads), a.smem_bytes, st, 1, a);
+}
+
+}  // namespace li

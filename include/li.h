@@ -534,9 +534,11 @@ LI_API li_status li_latent_attention(li_ctx* ctx, const li_paged_cache* cache, c
  * [cu_q[b], cu_q[b+1]) and keys [cu_k[b], cu_k[b+1]).  Query i of nq attends
  * the keys j <= i + nk - nq with causal != 0 (the last query sees all nk
  * keys), all nk keys without; scale, out and lse as li_latent_attention (a
- * query that attends nothing: 0 and -inf).
- * Strides are in elements, every row 16-byte aligned; a token's row of a
- * head is contiguous.  q rows hold d_nope + d_rope elements.
+ * query that attends nothing: 0 and -inf).  A sequence's keys and values must
+ * be finite, also where causality hides them; rows of no sequence may hold
+ * anything.
+ * Strides are in elements and positive, every row 16-byte aligned; a token's
+ * row of a head is contiguous.  q rows hold d_nope + d_rope elements.
  * cu_q, cu_k [batch + 1] int32 device, non-decreasing from 0; values are
  * clamped to [0, total_q] and [0, total_k], and rows of out and lse outside
  * [cu_q[0], cu_q[batch]) are left as they were.  max_q: at least the longest
