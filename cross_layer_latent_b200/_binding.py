@@ -390,6 +390,7 @@ def li_attention_recall(ctx: Context, probs: torch.Tensor, sel: torch.Tensor, K:
 # ---------------------------------------------------------------- attention over the selected tokens
 
 _NORM = {"none": 0, "rms": 1, "layer": 2}
+_raw_stream = torch._C._cuda_getCurrentRawStream if hasattr(torch._C, "_cuda_getCurrentRawStream") else None
 
 
 def _need(ok: bool, status: str, message: str):
@@ -398,24 +399,43 @@ def _need(ok: bool, status: str, message: str):
         raise LiError(STATUS[status], message)
 
 
-def _check_tensor(name: str, t: Optional[torch.Tensor], shape, dtype, ctx: Context, contiguous: bool = True):
-    if t is None:
-        return
-    _need(tuple(t.shape) == tuple(shape), "LI_ERR_SHAPE", f"{name} is {tuple(t.shape)}, expected {tuple(shape)}")
-    _need(t.dtype == dtype, "LI_ERR_DTYPE", f"{name} is {t.dtype}, expected {dtype}")
-    _need(t.device.type != "cuda" or t.device.index == ctx.device, "LI_ERR_ARG",
-          f"{name} is on {t.device}, the context on device {ctx.device}")
+def _check_tensor(name: str, t: torch.Tensor, shape, dtype, device: int, contiguous: bool = True):
+    """Explains what is wrong with a tensor (calls are made once per launch, so the passing path is kept short)."""
+    _need(t.shape == shape, "LI_ERR_SHAPE", f"{name} is {tuple(t.shape)}, expected {tuple(shape)}")
+    _need(t.dtype is dtype, "LI_ERR_DTYPE", f"{name} is {t.dtype}, expected {dtype}")
+    _need(t.get_device() == device, "LI_ERR_ARG", f"{name} is on {t.device}, expected device {device}")
     _need(t.is_contiguous() if contiguous else t.shape[-1] <= 1 or t.stride(-1) == 1, "LI_ERR_ARG",
           f"{name} must be contiguous" if contiguous else f"rows of {name} must be contiguous")
 
 
-@dataclass
+def _in(name: str, t: Optional[torch.Tensor], shape, dtype, device: int):
+    """Address of a contiguous tensor of this shape and type (None: NULL)."""
+    if t is None:
+        return None
+    if t.shape != shape or t.dtype is not dtype or not t.is_contiguous() or t.get_device() != device:
+        _check_tensor(name, t, shape, dtype, device)
+    return t.data_ptr()
+
+
+def _current_stream(ctx, stream):
+    if stream is None and _raw_stream is not None:
+        return _raw_stream(ctx.device)
+    return _stream(stream)
+
+
+def _attn_dtype(t: torch.Tensor) -> int:
+    _need(t.dtype in (torch.float32, torch.bfloat16), "LI_ERR_DTYPE", f"float32 or bfloat16 only (got {t.dtype})")
+    return _DTYPE_CODE[t.dtype]
+
+
+@dataclass(frozen=True)
 class RowTransform:
     """Transforms of one row (li_row_transform): a norm ("none", "rms" or
     "layer") of elements [norm_offset, norm_offset + norm_dim) with optional
     gamma / beta [norm_dim] float32, then the rotation of [rope_offset,
     rope_offset + rope_dim) by inv_freq [rope_dim / 2] float32, slots being
-    adjacent pairs or, with rope_halves, element p and p + rope_dim / 2."""
+    adjacent pairs or, with rope_halves, element p and p + rope_dim / 2.  The C
+    record is made here, once: build a new one to change anything."""
     norm: str = "none"
     norm_offset: int = 0
     norm_dim: int = 0
@@ -427,58 +447,64 @@ class RowTransform:
     rope_halves: bool = False
     inv_freq: Optional[torch.Tensor] = None
 
-    def c(self, ctx: Context) -> c_li_row_transform:
+    def __post_init__(self):
         _need(self.norm in _NORM, "LI_ERR_ARG", f"unknown norm {self.norm!r}")
-        for name in ("gamma", "beta"):
-            _check_tensor(name, getattr(self, name), (self.norm_dim,), torch.float32, ctx)
-        if self.rope_dim:
-            _check_tensor("inv_freq", self.inv_freq, (self.rope_dim // 2,), torch.float32, ctx)
-        return c_li_row_transform(_NORM[self.norm], self.norm_offset, self.norm_dim, _ptr(self.gamma), _ptr(self.beta),
-                                  float(self.eps), self.rope_offset, self.rope_dim, 1 if self.rope_halves else 0,
-                                  _ptr(self.inv_freq))
+        tensors = [t for t in (self.gamma, self.beta, self.inv_freq if self.rope_dim else None) if t is not None]
+        device = tensors[0].get_device() if tensors else None
+        g, b = (_in(n, t, (self.norm_dim,), torch.float32, device) for n, t in (("gamma", self.gamma), ("beta", self.beta)))
+        f = _in("inv_freq", self.inv_freq, (self.rope_dim // 2,), torch.float32, device) if self.rope_dim else None
+        object.__setattr__(self, "device", device)
+        object.__setattr__(self, "c", c_li_row_transform(_NORM[self.norm], self.norm_offset, self.norm_dim, g, b,
+                                                         float(self.eps), self.rope_offset, self.rope_dim,
+                                                         1 if self.rope_halves else 0, f))
 
 
-@dataclass
+@dataclass(frozen=True)
 class HeadRows:
     """The heads of every token in one tensor (li_head_rows): x [n_tok, H,
     dim] and out of the same shape, any strides over tokens and heads; out
-    may be x."""
+    may be x.  The C record is made here, once."""
     x: torch.Tensor
     tf: RowTransform
     out: torch.Tensor
 
-    def c(self, ctx: Context) -> c_li_head_rows:
-        _need(self.x.dim() == 3, "LI_ERR_SHAPE", f"x is {tuple(self.x.shape)}, expected [n_tok, H, dim]")
-        n, H, dim = self.x.shape
-        _check_tensor("x", self.x, (n, H, dim), self.x.dtype, ctx, contiguous=False)
-        _check_tensor("out", self.out, (n, H, dim), self.x.dtype, ctx, contiguous=False)
-        return c_li_head_rows(_ptr(self.x), _ptr(self.out), H, dim, self.x.stride(0), self.x.stride(1),
-                              self.out.stride(0), self.out.stride(1), self.tf.c(ctx))
+    def __post_init__(self):
+        x, out = self.x, self.out
+        _need(x.dim() == 3, "LI_ERR_SHAPE", f"x is {tuple(x.shape)}, expected [n_tok, H, dim]")
+        device = x.get_device()
+        _check_tensor("x", x, x.shape, x.dtype, device, contiguous=False)
+        _check_tensor("out", out, x.shape, x.dtype, device, contiguous=False)
+        _need(self.tf.device in (None, device), "LI_ERR_ARG", f"the transform is on device {self.tf.device}, x on {device}")
+        object.__setattr__(self, "dtype", _attn_dtype(x))
+        object.__setattr__(self, "device", device)
+        object.__setattr__(self, "n", x.shape[0])
+        object.__setattr__(self, "c", c_li_head_rows(x.data_ptr(), out.data_ptr(), x.shape[1], x.shape[2], x.stride(0),
+                                                     x.stride(1), out.stride(0), out.stride(1), self.tf.c))
 
 
-@dataclass
+_HEAD_ROWS = {n: c_li_head_rows * n for n in (1, 2, 3, 4)}
+
+
+@dataclass(frozen=True)
 class PagedCache:
     """A paged cache of attention latents (li_paged_cache): data [n_pages,
     page_size, dim] float32 or bfloat16, page_table [batch, max_pages] int32,
-    lengths [batch] int32."""
+    lengths [batch] int32.  The C record is made here, once."""
     data: torch.Tensor
     page_table: torch.Tensor
     lengths: torch.Tensor
 
-    def c(self, ctx: Context) -> c_li_paged_cache:
+    def __post_init__(self):
         _need(self.data.dim() == 3 and self.page_table.dim() == 2, "LI_ERR_SHAPE",
               "data must be [n_pages, page_size, dim] and page_table [batch, max_pages]")
         (n_pages, page, dim), (batch, max_pages) = self.data.shape, self.page_table.shape
-        _check_tensor("data", self.data, (n_pages, page, dim), self.data.dtype, ctx)
-        _check_tensor("page_table", self.page_table, (batch, max_pages), torch.int32, ctx)
-        _check_tensor("lengths", self.lengths, (batch,), torch.int32, ctx)
-        return c_li_paged_cache(_ptr(self.data), _ptr(self.page_table), _ptr(self.lengths), batch, n_pages, page,
-                                max_pages, dim, _attn_dtype(self.data))
-
-
-def _attn_dtype(t: torch.Tensor) -> int:
-    _need(t.dtype in (torch.float32, torch.bfloat16), "LI_ERR_DTYPE", f"float32 or bfloat16 only (got {t.dtype})")
-    return _DTYPE_CODE[t.dtype]
+        device = self.data.get_device()
+        c = c_li_paged_cache(_in("data", self.data, self.data.shape, self.data.dtype, device),
+                             _in("page_table", self.page_table, (batch, max_pages), torch.int32, device),
+                             _in("lengths", self.lengths, (batch,), torch.int32, device), batch, n_pages, page, max_pages,
+                             dim, _attn_dtype(self.data))
+        for name, v in (("c", c), ("ref", ctypes.byref(c)), ("device", device), ("batch", batch), ("dim", dim)):
+            object.__setattr__(self, name, v)
 
 
 def li_attention_workspace_bytes(ctx: Optional[Context], H: int, d_v: int) -> int:
@@ -492,16 +518,22 @@ def attention_workspace(ctx: Context, H: int, d_v: int, device=None) -> torch.Te
     return torch.zeros(li_attention_workspace_bytes(ctx, H, d_v), dtype=torch.uint8, device=device or f"cuda:{ctx.device}")
 
 
+def _workspace(ctx: Context, ws: torch.Tensor):
+    _need(ws.get_device() == ctx.device and ws.dtype is torch.uint8 and ws.is_contiguous(), "LI_ERR_WORKSPACE",
+          f"the workspace must be contiguous uint8 on device {ctx.device}")
+    return ws.data_ptr(), ws.numel()
+
+
 def li_norm_rope(ctx: Context, sets: List[HeadRows], pos: Optional[torch.Tensor] = None, stream=None):
     """Norms and rotation of the heads in every tensor of `sets` (1 to 4, the
     same tokens and type), pos [n_tok] int32, in one launch."""
     _need(1 <= len(sets) <= 4, "LI_ERR_ARG", f"need 1 to 4 tensors (got {len(sets)})")
-    n = sets[0].x.shape[0]
+    n, dtype = sets[0].n, sets[0].dtype
     for s in sets:
-        _need(s.x.shape[0] == n and s.x.dtype == sets[0].x.dtype, "LI_ERR_SHAPE", "the tensors differ in tokens or type")
-    _check_tensor("pos", pos, (n,), torch.int32, ctx)
-    arr = (c_li_head_rows * len(sets))(*[s.c(ctx) for s in sets])
-    ctx.check(_lib.li_norm_rope(ctx.handle, arr, len(sets), _attn_dtype(sets[0].x), n, _ptr(pos), _stream(stream)))
+        _need(s.n == n and s.dtype == dtype, "LI_ERR_SHAPE", "the tensors differ in tokens or type")
+        _need(s.device == ctx.device, "LI_ERR_ARG", f"a tensor is on device {s.device}, the context on {ctx.device}")
+    ctx.check(_lib.li_norm_rope(ctx.handle, _HEAD_ROWS[len(sets)](*[s.c for s in sets]), len(sets), dtype, n,
+                                _in("pos", pos, (n,), torch.int32, ctx.device), _current_stream(ctx, stream)))
 
 
 def li_append_paged(ctx: Context, cache: PagedCache, x: torch.Tensor, ws: torch.Tensor, tf: Optional[RowTransform] = None,
@@ -509,18 +541,19 @@ def li_append_paged(ctx: Context, cache: PagedCache, x: torch.Tensor, ws: torch.
     """x [batch, T, dim] (rows at one stride) into the cache, transformed, at
     positions start[b] (or lengths[b]) onwards; n_new [batch]: rows of each
     sequence."""
-    cc = cache.c(ctx)
+    dev, batch = ctx.device, cache.batch
+    _need(cache.device == dev and (tf is None or tf.device in (None, dev)), "LI_ERR_ARG",
+          f"the cache or the transform is not on the context's device {dev}")
     _need(x.dim() == 3, "LI_ERR_SHAPE", f"x is {tuple(x.shape)}, expected [batch, T, dim]")
     T = x.shape[1]
-    _check_tensor("x", x, (cc.batch, T, cc.dim), cache.data.dtype, ctx, contiguous=False)
+    if x.shape != (batch, T, cache.dim) or x.dtype is not cache.data.dtype or x.get_device() != dev or x.stride(2) != 1:
+        _check_tensor("x", x, (batch, T, cache.dim), cache.data.dtype, dev, contiguous=False)
     stride = x.stride(1) if T > 1 else x.stride(0)
-    _need(cc.batch == 1 or T == 0 or x.stride(0) == T * stride, "LI_ERR_ARG", "the rows of x must lie at one stride")
-    _check_tensor("start", start, (cc.batch,), torch.int32, ctx)
-    _check_tensor("n_new", n_new, (cc.batch,), torch.int32, ctx)
-    ct = tf.c(ctx) if tf is not None else None
-    ctx.check(_lib.li_append_paged(ctx.handle, ctypes.byref(cc), _ptr(x), T, stride,
-                                   ctypes.byref(ct) if ct is not None else None, _ptr(start), _ptr(n_new), _ptr(ws),
-                                   ws.numel(), _stream(stream)))
+    _need(batch == 1 or T == 0 or x.stride(0) == T * stride, "LI_ERR_ARG", "the rows of x must lie at one stride")
+    p, n = _workspace(ctx, ws)
+    ctx.check(_lib.li_append_paged(ctx.handle, cache.ref, x.data_ptr(), T, stride, tf.c if tf is not None else None,
+                                   _in("start", start, (batch,), torch.int32, dev),
+                                   _in("n_new", n_new, (batch,), torch.int32, dev), p, n, _current_stream(ctx, stream)))
 
 
 def li_latent_attention(ctx: Context, cache: PagedCache, q: torch.Tensor, d_v: int, scale: float, out: torch.Tensor,
@@ -529,21 +562,21 @@ def li_latent_attention(ctx: Context, cache: PagedCache, q: torch.Tensor, d_v: i
     """Absorbed queries q [batch, T, H, dim] over the cached latents: the
     positions of sel [batch, T, k] (a selection output), or the whole prefix.
     out [batch, T, H, d_v], lse [batch, T, H] float32, q_pos [batch, T]."""
-    cc = cache.c(ctx)
+    dev, b = ctx.device, cache.batch
+    _need(cache.device == dev, "LI_ERR_ARG", f"the cache is on device {cache.device}, the context on {dev}")
     _need(q.dim() == 4, "LI_ERR_SHAPE", f"q is {tuple(q.shape)}, expected [batch, T, H, dim]")
     _, T, H, _ = q.shape
     dt = cache.data.dtype
-    _check_tensor("q", q, (cc.batch, T, H, cc.dim), dt, ctx)
-    _check_tensor("out", out, (cc.batch, T, H, d_v), dt, ctx)
-    _check_tensor("lse", lse, (cc.batch, T, H), torch.float32, ctx)
-    _check_tensor("q_pos", q_pos, (cc.batch, T), torch.int32, ctx)
-    k = 0
+    k, sel_ptr = 0, None
     if sel is not None:
         k = sel.shape[-1]
         _need(k >= 1, "LI_ERR_SHAPE", "k must be >= 1 with sel")
-        _check_tensor("sel", sel, (cc.batch, T, k), torch.int32, ctx)
-    ctx.check(_lib.li_latent_attention(ctx.handle, ctypes.byref(cc), _ptr(q), T, H, int(d_v), float(scale), _ptr(q_pos),
-                                       _ptr(sel), k, _ptr(out), _ptr(lse), _ptr(ws), ws.numel(), _stream(stream)))
+        sel_ptr = _in("sel", sel, (b, T, k), torch.int32, dev)
+    p, n = _workspace(ctx, ws)
+    ctx.check(_lib.li_latent_attention(ctx.handle, cache.ref, _in("q", q, (b, T, H, cache.dim), dt, dev), T, H, d_v, scale,
+                                       _in("q_pos", q_pos, (b, T), torch.int32, dev), sel_ptr, k,
+                                       _in("out", out, (b, T, H, d_v), dt, dev),
+                                       _in("lse", lse, (b, T, H), torch.float32, dev), p, n, _current_stream(ctx, stream)))
 
 
 def li_prompt_attention(ctx: Context, q: torch.Tensor, k_nope: torch.Tensor, k_rope: Optional[torch.Tensor],
@@ -552,27 +585,26 @@ def li_prompt_attention(ctx: Context, q: torch.Tensor, k_nope: torch.Tensor, k_r
                         stream=None):
     """Expanded attention of a ragged batch of prompts: q [total_q, H, d_nope +
     d_rope], k_nope [total_k, H, d_nope], k_rope [total_k, d_rope] (shared by
-    the heads) or None, v [total_k, H, d_v], any strides over tokens and
-    heads; cu_q, cu_k [batch + 1] int32; out [total_q, H, d_v], lse
+    the heads) or None, v [total_k, H, d_v], any positive strides over tokens
+    and heads; cu_q, cu_k [batch + 1] int32; out [total_q, H, d_v], lse
     [total_q, H] float32."""
     _need(q.dim() == 3 and k_nope.dim() == 3 and v.dim() == 3, "LI_ERR_SHAPE", "q, k_nope and v must be [tokens, H, dim]")
-    (tq, H, dq), (tk, _, dn), dv = q.shape, k_nope.shape, v.shape[-1]
+    (tq, H, dq), (tk, _, dn), dv, dt, dev = q.shape, k_nope.shape, v.shape[-1], q.dtype, ctx.device
     dr = 0 if k_rope is None else k_rope.shape[-1]
-    batch = cu_q.numel() - 1
-    _check_tensor("q", q, (tq, H, dn + dr), q.dtype, ctx, contiguous=False)
-    _check_tensor("k_nope", k_nope, (tk, H, dn), q.dtype, ctx, contiguous=False)
-    _check_tensor("k_rope", k_rope, (tk, dr), q.dtype, ctx, contiguous=False)
-    _check_tensor("v", v, (tk, H, dv), q.dtype, ctx, contiguous=False)
-    _check_tensor("cu_q", cu_q, (batch + 1,), torch.int32, ctx)
-    _check_tensor("cu_k", cu_k, (batch + 1,), torch.int32, ctx)
-    _check_tensor("out", out, (tq, H, dv), q.dtype, ctx)
-    _check_tensor("lse", lse, (tq, H), torch.float32, ctx)
-    p = c_li_prompt(_ptr(q), _ptr(k_nope), _ptr(k_rope), _ptr(v), _attn_dtype(q), H, dn, dr, dv, tq, tk, batch, int(max_q),
-                    q.stride(0), q.stride(1), k_nope.stride(0), k_nope.stride(1),
-                    0 if k_rope is None else k_rope.stride(0), v.stride(0), v.stride(1), _ptr(cu_q), _ptr(cu_k),
-                    float(scale), 1 if causal else 0)
-    ctx.check(_lib.li_prompt_attention(ctx.handle, ctypes.byref(p), _ptr(out), _ptr(lse), _ptr(ws), ws.numel(),
-                                       _stream(stream)))
+    for name, t, shape in (("q", q, (tq, H, dn + dr)), ("k_nope", k_nope, (tk, H, dn)), ("v", v, (tk, H, dv)),
+                           ("k_rope", k_rope, (tk, dr))):
+        if t is not None and (t.shape != shape or t.dtype is not dt or t.get_device() != dev or t.stride(-1) != 1):
+            _check_tensor(name, t, shape, dt, dev, contiguous=False)
+    qs, ks, vs = q.stride(), k_nope.stride(), v.stride()
+    batch = cu_q.shape[0] - 1
+    rec = c_li_prompt(q.data_ptr(), k_nope.data_ptr(), None if k_rope is None else k_rope.data_ptr(), v.data_ptr(),
+                      _attn_dtype(q), H, dn, dr, dv, tq, tk, batch, max_q, qs[0], qs[1], ks[0], ks[1],
+                      0 if k_rope is None else k_rope.stride(0), vs[0], vs[1],
+                      _in("cu_q", cu_q, (batch + 1,), torch.int32, dev), _in("cu_k", cu_k, (batch + 1,), torch.int32, dev),
+                      scale, 1 if causal else 0)
+    p, n = _workspace(ctx, ws)
+    ctx.check(_lib.li_prompt_attention(ctx.handle, rec, _in("out", out, (tq, H, dv), dt, dev),
+                                       _in("lse", lse, (tq, H), torch.float32, dev), p, n, _current_stream(ctx, stream)))
 
 
 def li_set_trace(ctx: Context, buf: Optional[torch.Tensor]):

@@ -8,6 +8,8 @@ a product and one a sum), which moves a softmax weight relatively by twice the
 scaled amount; bf16 weights are rounded by H(bf16) more; exp2 and the scaling add
 2^-20.  All of that weighs on sum p |v|, which `attend` returns.
 """
+import dataclasses
+
 import numpy as np
 import pytest
 import torch
@@ -128,7 +130,7 @@ def test_norm_rope_several_sets(ctx):
     fused = rand(n, (8 + 2 + 1) * 128, dtype=BF, seed=2).to(DEV)
     q, k, ix = fused[:, :1024].unflatten(1, (8, 128)), fused[:, 1024:1280].unflatten(1, (2, 128)), fused[:, 1280:].unflatten(1, (2, 64))
     tfs = [make_tf(128, "rms", 64, False, 1), make_tf(128, "layer", 64, True, 2, beta=True), make_tf(64, "none", 64, False, 3)]
-    tfs[1].inv_freq = tfs[0].inv_freq          # shared frequencies
+    tfs[1] = dataclasses.replace(tfs[1], inv_freq=tfs[0].inv_freq)          # shared frequencies
     outs = [torch.empty(t.shape, dtype=BF, device=DEV) for t in (q, k, ix)]
     li.li_norm_rope(ctx, [li.HeadRows(x, tf, o) for x, tf, o in zip((q, k, ix), tfs, outs)], pos)
     for x, tf, o in zip((q, k, ix), tfs, outs):
@@ -549,17 +551,18 @@ def refusals(ctx, dev, stream):
     nr = lambda x, t, o=None, pos=i(2): li.li_norm_rope(ctx, [li.HeadRows(x, t, x if o is None else o)], pos, stream=stream)  # noqa: E731
     x = z(2, 3, 64)
     refused("LI_ERR_ARG", li.li_norm_rope, ctx, [], i(2), stream=stream)
-    refused("LI_ERR_DTYPE", nr, z(2, 3, 64, dtype=torch.float16), tf())
+    refused("LI_ERR_DTYPE", li.HeadRows, z(2, 3, 64, dtype=torch.float16), tf(), z(2, 3, 64, dtype=torch.float16))
     refused("LI_ERR_SHAPE", nr, x, tf(norm="rms", norm_offset=1, norm_dim=64))
     refused("LI_ERR_SHAPE", nr, x, tf(norm="rms"))
     refused("LI_ERR_ARG", nr, x, tf(norm="rms", norm_dim=64, eps=float("nan")))
-    refused("LI_ERR_ARG", nr, x, tf(norm="batch", norm_dim=64))
+    refused("LI_ERR_ARG", tf, norm="batch", norm_dim=64)
     refused("LI_ERR_SHAPE", nr, x, tf(rope_dim=63, inv_freq=z(31, dtype=F32)))
+    refused("LI_ERR_SHAPE", tf, rope_dim=64, inv_freq=z(31, dtype=F32))
     refused("LI_ERR_SHAPE", nr, x, tf(rope_offset=2, rope_dim=64, inv_freq=f))
     refused("LI_ERR_ARG", nr, x, tf(rope_dim=64))
     refused("LI_ERR_ARG", nr, x, tf(rope_dim=64, inv_freq=f), None, None)
     refused("LI_ERR_SHAPE", nr, z(2, 1, 1025), tf())
-    refused("LI_ERR_SHAPE", nr, x, tf(), z(2, 3, 32))
+    refused("LI_ERR_SHAPE", li.HeadRows, x, tf(), z(2, 3, 32))
     cache = lambda d=z(4, 8, 64), t=i(2, 2), n=i(2): li.PagedCache(d, t, n)  # noqa: E731
     ap = lambda c, x, w=ws, **k: li.li_append_paged(ctx, c, x, w, stream=stream, **k)  # noqa: E731
     refused("LI_ERR_SHAPE", ap, cache(), z(2, 0, 64))
@@ -584,7 +587,8 @@ def refusals(ctx, dev, stream):
     refused("LI_ERR_SHAPE", la, cache(), q, sel=i(2, 2, 8))
     refused("LI_ERR_ARG", la, cache(), q, 32, float("inf"))
     refused("LI_ERR_DTYPE", la, cache(), q, out=z(2, 1, 4, 32, dtype=F32))
-    refused("LI_ERR_DTYPE", la, cache(z(4, 8, 64, dtype=torch.uint8)), z(2, 1, 4, 64, dtype=torch.uint8))
+    refused("LI_ERR_DTYPE", cache, z(4, 8, 64, dtype=torch.uint8))
+    refused("LI_ERR_SHAPE", cache, z(4, 8, 64), i(2, 2), i(3))
     refused("LI_ERR_ARG", la, cache(), z(2, 1, 4, 128)[..., :64])
     refused("LI_ERR_WORKSPACE", la, cache(), q, w=ws_big[:128])
     pa = lambda q, kn, kr, v, cq=i(3), ck=i(3), out=None, w=ws_big, scale=1.0, m=4: li.li_prompt_attention(  # noqa: E731
