@@ -190,6 +190,7 @@ li_status latent_mma(li_ctx* c, const li_paged_cache* cache, const void* q, int 
   const char* what = "li_latent_attention";
   LatentMmaArgs a;
   memset(&a, 0, sizeof(a));
+  a.data = cache->data;
   a.page_table = cache->page_table;
   a.lengths = cache->lengths;
   a.q_pos = q_pos;
@@ -212,10 +213,10 @@ li_status latent_mma(li_ctx* c, const li_paged_cache* cache, const void* q, int 
   a.n_pages = cache->n_pages;
   a.page_size = cache->page_size;
   a.max_pages = cache->max_pages;
-  a.pool_rows = cache->n_pages * cache->page_size;
-  // whole boxes of rows where pages hold them (the 128-byte swizzle repeats every 8 rows)
-  a.box = 32;
-  while (cache->page_size % a.box) a.box /= 2;
+  // whole boxes of rows where a page holds them (the 128-byte swizzle repeats every 8 rows); selected rows come
+  // one by one
+  a.box = sel ? 0 : 32;
+  while (a.box && cache->page_size % a.box) a.box /= 2;
   if (a.box < 8) a.box = 0;
   if (!latent_mma_layout(&a, c->num_sms, c->max_smem_optin))
     return fail(c, LI_ERR_UNSUPPORTED, "%s: operands too large for shared memory (dim %d)", what, a.dim);
@@ -225,12 +226,12 @@ li_status latent_mma(li_ctx* c, const li_paged_cache* cache, const void* q, int 
   const cuuint32_t qbox[3] = {64, static_cast<cuuint32_t>(a.N), 1};
   li_status s = encode_map(c, &a.map_q, LI_BF16, 3, const_cast<void*>(q), qdims, qstr, qbox, 128);
   if (s != LI_OK) return s;
-  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(a.dim), static_cast<cuuint64_t>(a.pool_rows)};
-  const cuuint64_t str[1] = {row_bytes};
-  const cuuint32_t one[2] = {64, 1}, box[2] = {64, static_cast<cuuint32_t>(a.box)};
-  if ((s = encode_map(c, &a.map_rows, LI_BF16, 2, cache->data, dims, str, one, 128, false)) != LI_OK) return s;
-  if (a.box && !sel && (s = encode_map(c, &a.map_box, LI_BF16, 2, cache->data, dims, str, box, 128)) != LI_OK) return s;
-  if (sel) a.box = 0;
+  if (a.box) {
+    const cuuint64_t dims[2] = {static_cast<cuuint64_t>(a.dim), static_cast<cuuint64_t>(cache->n_pages) * cache->page_size};
+    const cuuint64_t str[1] = {row_bytes};
+    const cuuint32_t box[2] = {64, static_cast<cuuint32_t>(a.box)};
+    if ((s = encode_map(c, &a.map_box, LI_BF16, 2, cache->data, dims, str, box, 128)) != LI_OK) return s;
+  }
   (void)cudaGetLastError();
   {
     Launch L(c, st, "latent_attn", a.grid, 416, static_cast<int>(a.smem_bytes));

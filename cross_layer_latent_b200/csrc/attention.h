@@ -60,8 +60,8 @@ struct LatentAttnArgs {
 // bf16 on the tensor cores (latent_mma.cu).
 struct alignas(64) LatentMmaArgs {
   CUtensorMap map_q;      // queries: dims {dim, rows, seqs}, box {64, N, 1}
-  CUtensorMap map_rows;   // pool rows one by one: dims {dim, pool_rows}, box {64, 1} (gathers of four)
-  CUtensorMap map_box;    // pool rows of a page: box {64, box}
+  CUtensorMap map_box;    // pool rows: dims {dim, pool rows}, box {64, box}
+  const void* data;
   const int32_t* page_table;
   const int32_t* lengths;
   const int32_t* q_pos;
@@ -76,8 +76,8 @@ struct alignas(64) LatentMmaArgs {
   int seqs;               // work units with rows of their own: sequences, with sel (sequence, query) pairs
   int rows;               // query rows of a unit: T * H, with sel H
   int T, H, k, dim, d_v;
-  int n_pages, page_size, max_pages, pool_rows;
-  int box;                // rows of a box (a divisor of the page size), 0: gather always
+  int n_pages, page_size, max_pages;
+  int box;                // rows of a box (a divisor of the page size), 0: rows one by one always
   // filled by latent_mma_layout
   int N, groups;          // MMA columns, groups of N rows in a unit
   int nb, last_ksteps;    // 64-column blocks of a row, 16-element K steps of the last one

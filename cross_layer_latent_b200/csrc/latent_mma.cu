@@ -48,8 +48,8 @@ constexpr float kNoMax = -1e30f;
 constexpr uint64_t kDrainNs = 1000ull * 1000ull;
 
 struct Smem {
-  uint64_t full[kMaxBufs][kMaxBlocks];           // block arrived
-  uint64_t empty[kMaxBufs][kMaxBlocks / 2];      // two blocks free again
+  uint64_t full[kMaxBufs][kMaxBlocks / 2];       // two blocks (a pair) arrived
+  uint64_t empty[kMaxBufs][kMaxBlocks / 2];      // they are free again
   uint64_t meta[kMaxBufs];                       // tokens' valid bits written
   uint64_t q_full, q_empty, s_full[2], p_full[2], pv_done, o_full, o_empty, drain;
   uint32_t tmem;
@@ -169,6 +169,28 @@ struct Walk {
   }
 };
 
+// Position in the ring of tile buffers, and the phase of its barriers.
+struct Ring {
+  int buf = 0;
+  uint32_t ph = 0;
+  __device__ __forceinline__ void step(int bufs) {
+    if (++buf == bufs) {
+      buf = 0;
+      ph ^= 1u;
+    }
+  }
+};
+
+// Arrives `n` times at once.
+__device__ __forceinline__ void mbar_arrive_n(uint64_t* bar, uint32_t n) {
+  asm volatile("mbarrier.arrive.release.cta.shared::cta.b64 _, [%0], %1;" ::"r"(smem_addr(bar)), "r"(n) : "memory");
+}
+
+// 16 bytes from global to shared memory, zeros where src_bytes is 0.
+__device__ __forceinline__ void cp_async_16_or_zero(uint32_t dst, const void* src, uint32_t src_bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(src_bytes) : "memory");
+}
+
 template <int N>
 __global__ void __launch_bounds__(kThreads, 1) latent_mma_kernel(const __grid_constant__ LatentMmaArgs a) {
   extern __shared__ uint8_t raw[];
@@ -183,8 +205,10 @@ __global__ void __launch_bounds__(kThreads, 1) latent_mma_kernel(const __grid_co
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < a.bufs; ++i) {
-      for (int j = 0; j < a.nb; ++j) mbar_init(&sm.full[i][j], kLoadWarps);
-      for (int j = 0; j < pairs; ++j) mbar_init(&sm.empty[i][j], 1);
+      for (int j = 0; j < pairs; ++j) {
+        mbar_init(&sm.full[i][j], 32 * kLoadWarps);
+        mbar_init(&sm.empty[i][j], 1);
+      }
       mbar_init(&sm.meta[i], kLoadWarps);
     }
     mbar_init(&sm.q_full, 1);
@@ -200,7 +224,6 @@ __global__ void __launch_bounds__(kThreads, 1) latent_mma_kernel(const __grid_co
     sm.abort_flag = 0;
     fence_barrier_init();
     tma_prefetch_desc(&a.map_q);
-    tma_prefetch_desc(&a.map_rows);
     if (a.box) tma_prefetch_desc(&a.map_box);
   }
   if (warp == kMmaWarp) {
@@ -232,7 +255,8 @@ __global__ void __launch_bounds__(kThreads, 1) latent_mma_kernel(const __grid_co
     const int c0 = wg * CW;                      // first column
     const int bar = 1 + wg;
     Walk w;
-    int64_t tile = 0, seg = 0;                   // counted over the CTA's share
+    Ring ring, sring;                            // tile buffers, score buffers
+    uint32_t tile = 0, seg = 0;                  // parities over the CTA's share
     bool dead = false;
     for (bool more = w.start(a, sm); more && !dead; more = w.next(a), ++seg) {
       const int r0 = w.s.g * N;                  // first query row of the group
@@ -249,12 +273,11 @@ __global__ void __launch_bounds__(kThreads, 1) latent_mma_kernel(const __grid_co
 #pragma unroll
       for (int i = 0; i < CW; ++i) sum[i] = 0.f;
       for (int t = w.s.t0; t < w.s.t1; ++t, ++tile) {
-        const int buf = static_cast<int>(tile % a.bufs);
-        const uint32_t buf_phase = static_cast<uint32_t>(tile / a.bufs) & 1u;
-        const int sb = a.s_bufs == 2 ? static_cast<int>(tile & 1) : 0;
-        const uint32_t s_phase = static_cast<uint32_t>(a.s_bufs == 2 ? tile >> 1 : tile) & 1u;
-        bool ok = bounded_wait(&sm.meta[buf], buf_phase, wc);
-        ok = bounded_wait(&sm.s_full[sb], s_phase, wc) && ok;
+        const int buf = ring.buf, sb = sring.buf;
+        bool ok = bounded_wait(&sm.meta[buf], ring.ph, wc);
+        ok = bounded_wait(&sm.s_full[sb], sring.ph, wc) && ok;
+        ring.step(a.bufs);
+        sring.step(a.s_bufs);
         __syncwarp();
         tc_fence_after();
         uint32_t xr[CW];
@@ -303,7 +326,7 @@ __global__ void __launch_bounds__(kThreads, 1) latent_mma_kernel(const __grid_co
           }
           named_bar_sync(bar, 128);
           if (t > w.s.t0) {
-            ok = bounded_wait(&sm.pv_done, static_cast<uint32_t>(tile - 1) & 1u, wc);
+            ok = bounded_wait(&sm.pv_done, (tile - 1) & 1u, wc);
             if (named_bar_any(bar, 128, !ok)) {
               dead = true;
               break;
@@ -386,7 +409,7 @@ __global__ void __launch_bounds__(kThreads, 1) latent_mma_kernel(const __grid_co
           a.part_ml[(slot * 64 + c) * 2 + 1] = l;
         }
       }
-      bool ok = bounded_wait(&sm.o_full, static_cast<uint32_t>(seg) & 1u, wc);
+      bool ok = bounded_wait(&sm.o_full, seg & 1u, wc);
       if (named_bar_any(bar, 128, !ok)) {
         dead = true;
         break;
@@ -421,60 +444,66 @@ __global__ void __launch_bounds__(kThreads, 1) latent_mma_kernel(const __grid_co
       const uint32_t id_s = make_instr_desc(1, 128, N);
       const uint32_t id_o = id_s | kMajorMnA | kMajorMnB;
       Walk w;
-      int64_t tile = 0, seg = 0;
+      Ring sr, ssr, vr, vsr;                     // tile and score buffers of the next scores, of the next values
+      uint32_t seg = 0;
       bool ok = true;
-      // S^T of tile number i (of the CTA's share)
-      auto scores = [&](int64_t i) {
-        const int buf = static_cast<int>(i % a.bufs);
-        const uint32_t ph = static_cast<uint32_t>(i / a.bufs) & 1u;
-        const int sb = a.s_bufs == 2 ? static_cast<int>(i & 1) : 0;
-        const uint32_t d = s_tmem + sb * N;
-        const uint32_t blk0 = tiles_smem + buf * a.slots * kBlockBytes;
+      const uint64_t da0 = desc_sw128(tiles_smem, 16, 1024), db0 = desc_sw128(q_smem, 16, 1024);
+      const uint64_t dv0 = desc_sw128(tiles_smem, kBlockBytes, 1024);
+      constexpr uint64_t kBlockDesc = kBlockBytes >> 4, kQDesc = (N * 128) >> 4;
+      // S^T of the next tile
+      auto scores = [&]() {
+        const uint32_t d = s_tmem + ssr.buf * N;
+        uint64_t da = da0 + sr.buf * a.slots * kBlockDesc, db = db0;
         uint32_t acc = 0;
-        for (int j = 0; j < a.nb; ++j) {
-          if (!bounded_wait(&sm.full[buf][j], ph, wc)) return false;
+        for (int p = 0; p < pairs; ++p) {
+          const int nblk = min(2, a.nb - 2 * p);
+          if (nblk <= 0) break;
+          if (!bounded_wait(&sm.full[sr.buf][p], sr.ph, wc)) return false;
+          fence_proxy_async_smem();              // rows gathered by cp.async are read by the tensor cores
           tc_fence_after();
-          const uint64_t da = desc_sw128(blk0 + j * kBlockBytes, 16, 1024);
-          const uint64_t db = desc_sw128(q_smem + j * N * 128, 16, 1024);
-          const int ks = j == a.nb - 1 ? a.last_ksteps : 4;
+          for (int j = 0; j < nblk; ++j, da += kBlockDesc, db += kQDesc) {
+            const int ks = 2 * p + j == a.nb - 1 ? a.last_ksteps : 4;
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk) {
-            if (kk < ks) umma<kKindBF16>(d, da + 2 * kk, db + 2 * kk, id_s, acc);
-            acc = 1;
+            for (int kk = 0; kk < 4; ++kk) {
+              if (kk < ks) umma<kKindBF16>(d, da + 2 * kk, db + 2 * kk, id_s, acc);
+              acc = 1;
+            }
           }
         }
-        umma_commit(&sm.s_full[sb]);
+        umma_commit(&sm.s_full[ssr.buf]);
+        sr.step(a.bufs);
+        ssr.step(a.s_bufs);
         return true;
       };
       for (bool more = w.start(a, sm); more && ok; more = w.next(a), ++seg) {
-        if (!(ok = bounded_wait(&sm.q_full, static_cast<uint32_t>(seg) & 1u, wc))) break;
+        if (!(ok = bounded_wait(&sm.q_full, seg & 1u, wc))) break;
         const int nt = w.s.t1 - w.s.t0;
         const int ahead = a.s_bufs - 1;          // scores run one tile ahead where there are two buffers
         int issued = 0;
-        for (int t = 0; t < nt && ok; ++t, ++tile) {
+        for (int t = 0; t < nt && ok; ++t) {
           while (ok && issued < nt && issued <= t + ahead) {
-            ok = scores(tile - t + issued);
+            ok = scores();
             if (++issued == nt) umma_commit(&sm.q_empty);
           }
           if (!ok) break;
-          if (t == 0 && seg > 0 && !(ok = bounded_wait(&sm.o_empty, static_cast<uint32_t>(seg - 1) & 1u, wc))) break;
-          const int sb = a.s_bufs == 2 ? static_cast<int>(tile & 1) : 0;
-          const uint32_t s_phase = static_cast<uint32_t>(a.s_bufs == 2 ? tile >> 1 : tile) & 1u;
-          if (!(ok = bounded_wait(&sm.p_full[sb], s_phase, wc))) break;
+          if (t == 0 && seg > 0 && !(ok = bounded_wait(&sm.o_empty, (seg - 1) & 1u, wc))) break;
+          if (!(ok = bounded_wait(&sm.p_full[vsr.buf], vsr.ph, wc))) break;
           tc_fence_after();
-          const int buf = static_cast<int>(tile % a.bufs);
-          const uint32_t blk0 = tiles_smem + buf * a.slots * kBlockBytes;
-          const uint64_t dp = desc_sw128(blk0 + (a.slots - 1) * kBlockBytes, kBlockBytes, 1024);
+          const uint64_t dt = dv0 + vr.buf * a.slots * kBlockDesc;
+          const uint64_t dp = dt + (a.slots - 1) * kBlockDesc;
+          uint64_t* const empty = sm.empty[vr.buf];
           for (int mb = 0; mb < a.m_blocks; ++mb) {
-            const uint64_t dv = desc_sw128(blk0 + 2 * mb * kBlockBytes, kBlockBytes, 1024);
+            const uint64_t dv = dt + 2 * mb * kBlockDesc;
 #pragma unroll
             for (int kk = 0; kk < 8; ++kk)
               umma<kKindBF16>(o_tmem + mb * N, dv + kk * 128, dp + kk * 128, id_o, (t > 0 || kk > 0) ? 1u : 0u);
-            if (mb < a.m_blocks - 1) umma_commit(&sm.empty[buf][mb]);
+            if (mb < a.m_blocks - 1) umma_commit(&empty[mb]);
           }
-          for (int p = a.m_blocks - 1; p < pairs; ++p) umma_commit(&sm.empty[buf][p]);
+          for (int p = a.m_blocks - 1; p < pairs; ++p) umma_commit(&empty[p]);
           umma_commit(&sm.pv_done);
           if (t == nt - 1) umma_commit(&sm.o_full);
+          vr.step(a.bufs);
+          vsr.step(a.s_bufs);
         }
       }
       // nothing is in flight when the CTA ends, whichever role gave up
@@ -486,18 +515,22 @@ __global__ void __launch_bounds__(kThreads, 1) latent_mma_kernel(const __grid_co
     // ------------------------------------------------ loads
     const int lw = warp - kMmaWarp - 1;          // 32 tokens of every tile
     Walk w;
-    int64_t tile = 0, seg = 0, fetched = 0;
+    Ring ring;
+    uint32_t seg = 0, queries = 0;
+    int64_t tile = 0;
     bool ok = true;
+    const uint32_t my_rows = tiles_smem + lw * 32 * 128;
     for (bool more = w.start(a, sm); more && ok; more = w.next(a), ++seg) {
       // queries of the group (one lane), once the previous group's scores are done
       if (lw == 0) {
-        if (seg > 0) ok = __all_sync(0xffffffffu, bounded_wait(&sm.q_empty, static_cast<uint32_t>(seg - 1) & 1u, wc));
+        if (seg > 0) ok = __all_sync(0xffffffffu, bounded_wait(&sm.q_empty, (seg - 1) & 1u, wc));
         if (!ok) break;
         if (lane == 0) {
           mbar_arrive_expect_tx(&sm.q_full, a.nb * N * 128);
           for (int j = 0; j < a.nb; ++j)
             tma_load_3d(base + j * N * 128, &a.map_q, &sm.q_full, 64 * j, w.s.g * N, w.s.b);
         }
+        ++queries;
         __syncwarp();
       }
       // what the group's rows see at most; positions and pages of a tile are read two and one tiles ahead
@@ -531,60 +564,88 @@ __global__ void __launch_bounds__(kThreads, 1) latent_mma_kernel(const __grid_co
       int pg0 = page_of(s0);
       int s1 = position(w.s.t0 + 1);
       for (int t = w.s.t0; t < w.s.t1; ++t, ++tile) {
-        const int buf = static_cast<int>(tile % a.bufs);
-        const uint32_t use = static_cast<uint32_t>(tile / a.bufs);
+        const int buf = ring.buf;
+        const uint32_t free_phase = ring.ph ^ 1u;
+        ring.step(a.bufs);
         if (s0 >= 0 && (pg0 < 0 || pg0 >= a.n_pages)) {
           record_status(a.status, kStatusIndex);
           s0 = -1;
         }
-        // rows past the pool's end read as zeros: tokens that nobody attends
-        const int row = s0 >= 0 ? pg0 * a.page_size + s0 % a.page_size : a.pool_rows;
+        const int row = s0 >= 0 ? pg0 * a.page_size + s0 % a.page_size : -1;
         const unsigned valid = __ballot_sync(0xffffffffu, s0 >= 0);
-        const bool boxes = a.box && !sel && valid == 0xffffffffu;
+        const bool boxes = a.box && valid == 0xffffffffu;
         // next tile's pages, and the positions after that
         s0 = checked(s1);
         pg0 = page_of(s0);
         s1 = position(t + 2);
-        const uint32_t blk0 = tiles_smem + buf * a.slots * kBlockBytes + lw * 32 * 128;
-        for (int p = 0; p < pairs && ok; ++p) {
-          if (use > 0) ok = __all_sync(0xffffffffu, bounded_wait(&sm.empty[buf][p], (use - 1) & 1u, wc));
-          if (!ok) break;
-          if (p == 0 && lane == 0) {
-            sm.valid[buf][lw] = valid;
-            mbar_arrive(&sm.meta[buf]);
+        const uint32_t dst = my_rows + buf * a.slots * kBlockBytes;
+        const bool wait = tile >= a.bufs;
+        if (boxes) {
+          // lane i < 32 / box loads box i of every block
+          const int i = lane & (32 / a.box - 1);
+          const int r = __shfl_sync(0xffffffffu, row, i * a.box);
+          uint8_t* to = base + (dst - q_smem) + i * a.box * 128;
+          for (int p = 0; p < pairs && ok; ++p) {
+            const int nblk = min(2, a.nb - 2 * p);
+            if (wait) ok = __all_sync(0xffffffffu, bounded_wait(&sm.empty[buf][p], free_phase, wc));
+            if (!ok) break;
+            if (lane == 0) {
+              if (p == 0) {
+                sm.valid[buf][lw] = valid;
+                mbar_arrive(&sm.meta[buf]);
+              }
+              if (nblk > 0) {
+                mbar_arrive_n(&sm.full[buf][p], 31);
+                mbar_arrive_expect_tx(&sm.full[buf][p], nblk * 32 * 128);
+              }
+            }
+            if (lane < 32 / a.box)
+              for (int j = 2 * p; j < 2 * p + nblk; ++j) tma_load_2d(to + j * kBlockBytes, &a.map_box, &sm.full[buf][p], 64 * j, r);
           }
-          const int nblk = min(2, a.nb - 2 * p);
-          if (nblk <= 0) continue;
-          if (lane < nblk) mbar_arrive_expect_tx(&sm.full[buf][2 * p + lane], 32 * 128);
-          __syncwarp();
-          if (boxes) {
-            const int per = 32 / a.box;
-            const int j = 2 * p + lane / per, i = lane % per;
-            const int r = __shfl_sync(0xffffffffu, row, i * a.box);
-            if (lane < nblk * per)
-              tma_load_2d(base + (blk0 - q_smem) + j * kBlockBytes + i * a.box * 128, &a.map_box, &sm.full[buf][j], 64 * j, r);
-          } else {
-            const int j = 2 * p + (lane >> 3), i = (lane & 7) * 4;
-            const int ra = __shfl_sync(0xffffffffu, row, i), rb = __shfl_sync(0xffffffffu, row, i + 1);
-            const int rc = __shfl_sync(0xffffffffu, row, i + 2), rd = __shfl_sync(0xffffffffu, row, i + 3);
-            if (lane < nblk * 8) tma_gather4(blk0 + j * kBlockBytes + i * 128, &a.map_rows, &sm.full[buf][j], 64 * j, ra, rb, rc, rd);
+        } else {
+          // eight lanes a row, four rows at a time, in 16-byte pieces; tokens that nobody attends become zeros
+          const int c = lane & 7;
+          const uint8_t* src[8];
+          uint32_t there = 0;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const int r = __shfl_sync(0xffffffffu, row, 4 * i + (lane >> 3));
+            if (r >= 0) there |= 1u << i;
+            src[i] = static_cast<const uint8_t*>(a.data) + static_cast<int64_t>(max(r, 0)) * a.dim * 2 + c * 16;
           }
-          fetched = tile * pairs + p + 1;
+          // 128-byte swizzle: piece c of row r lies at c ^ (r mod 8); rows 4 i + lane / 8
+          const uint32_t even = dst + (lane >> 3) * 128 + ((c ^ (lane >> 3)) << 4);
+          const uint32_t odd = dst + (lane >> 3) * 128 + ((c ^ (4 + (lane >> 3))) << 4);
+          for (int p = 0; p < pairs && ok; ++p) {
+            const int nblk = min(2, a.nb - 2 * p);
+            if (wait) ok = __all_sync(0xffffffffu, bounded_wait(&sm.empty[buf][p], free_phase, wc));
+            if (!ok) break;
+            if (p == 0 && lane == 0) {
+              sm.valid[buf][lw] = valid;
+              mbar_arrive(&sm.meta[buf]);
+            }
+            if (nblk <= 0) continue;
+            for (int j = 2 * p; j < 2 * p + nblk; ++j) {
+              const bool in_row = 64 * j + c * 8 < a.dim;
+#pragma unroll
+              for (int i = 0; i < 8; ++i) {
+                const bool on = in_row && ((there >> i) & 1u);
+                cp_async_16_or_zero((i & 1 ? odd : even) + j * kBlockBytes + i * 512, on ? src[i] + j * 128 : static_cast<const uint8_t*>(a.data),
+                                    on ? 16u : 0u);
+              }
+            }
+            cp_async_arrive_noinc(&sm.full[buf][p]);
+          }
         }
         if (!ok) break;
       }
     }
-    if (fetched > 0) {
-      // the copies that were issued land before the CTA ends, whichever role gave up
-      const int64_t last = fetched - 1;
-      for (int64_t f = max(last - static_cast<int64_t>(a.bufs) * pairs + 1, int64_t(0)); f <= last; ++f) {
-        const int64_t i = f / pairs;
-        const int p = static_cast<int>(f % pairs);
-        for (int j = 2 * p; j < min(2 * p + 2, a.nb); ++j)
-          drain_wait(&sm.full[i % a.bufs][j], static_cast<uint32_t>(i / a.bufs) & 1u, kDrainNs);
-      }
-      if (lw == 0) drain_wait(&sm.q_full, static_cast<uint32_t>(ok ? seg - 1 : seg) & 1u, kDrainNs);
-    }
+    // the copies that were issued land before the CTA ends, whichever role gave up
+    cp_async_wait_all();
+    for (int64_t i = max(tile - a.bufs, int64_t(0)); i < tile; ++i)
+      for (int p = 0; 2 * p < a.nb; ++p)
+        drain_wait(&sm.full[i % a.bufs][p], static_cast<uint32_t>(i / a.bufs) & 1u, kDrainNs);
+    if (lw == 0 && queries > 0) drain_wait(&sm.q_full, (queries - 1) & 1u, kDrainNs);
   }
   tc_fence_before();
   __syncthreads();
@@ -610,22 +671,40 @@ __global__ void __launch_bounds__(128) latent_join_kernel(const __grid_constant_
   if (((first + 1) * n - 1) / total != i0) return;
   const int64_t i1 = ((last + 1) * n - 1) / total;
   auto slot = [&](int64_t i) { return 2 * i + (i == i0 ? 1 : 0); };
-  float M = kNoMax, L = 0.f;
-  for (int64_t i = i0; i <= i1; ++i) M = fmaxf(M, a.part_ml[(slot(i) * 64 + c) * 2]);
   const int d = threadIdx.x * 4;
+  float M = kNoMax, L = 0.f;
   float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-  for (int64_t i = i0; i <= i1; ++i) {
-    const int64_t r = slot(i) * 64 + c;
-    const float2 ml = *reinterpret_cast<const float2*>(a.part_ml + r * 2);
-    const float f = exp2_fast(ml.x - M);
-    L = fmaf(f, ml.y, L);
-    if (d < a.d_v) {
-      const float4 v = *reinterpret_cast<const float4*>(a.part_o + r * a.part_stride + d);
-      s.x = fmaf(f, v.x, s.x);
-      s.y = fmaf(f, v.y, s.y);
-      s.z = fmaf(f, v.z, s.z);
-      s.w = fmaf(f, v.w, s.w);
+  for (int64_t j0 = i0; j0 <= i1; j0 += 32) {
+    // the maxima and sums of 32 parts, one a lane; what came before is rescaled to the new maximum
+    const int cnt = static_cast<int>(min(i1 - j0 + 1, int64_t(32)));
+    float2 ml = make_float2(kNoMax, 0.f);
+    if (lane < cnt) ml = *reinterpret_cast<const float2*>(a.part_ml + (slot(j0 + lane) * 64 + c) * 2);
+    const float now = fmaxf(M, warp_max_f32(ml.x));
+    const float keep = exp2_fast(M - now), mine = exp2_fast(ml.x - now);
+    M = now;
+    float l = mine * ml.y;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+    L = fmaf(L, keep, l);
+    s.x *= keep;
+    s.y *= keep;
+    s.z *= keep;
+    s.w *= keep;
+    for (int j1 = 0; j1 < cnt; j1 += 8) {
+      float4 v[8];
+#pragma unroll
+      for (int u = 0; u < 8; ++u)
+        if (d < a.d_v && j1 + u < cnt) v[u] = *reinterpret_cast<const float4*>(a.part_o + (slot(j0 + j1 + u) * 64 + c) * a.part_stride + d);
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        const float f = __shfl_sync(0xffffffffu, mine, j1 + u);
+        if (d < a.d_v && j1 + u < cnt) {
+          s.x = fmaf(f, v[u].x, s.x);
+          s.y = fmaf(f, v[u].y, s.y);
+          s.z = fmaf(f, v[u].z, s.z);
+          s.w = fmaf(f, v[u].w, s.w);
+        }
+      }
     }
   }
   const int64_t row = static_cast<int64_t>(p.b) * a.rows + p.g * a.N + c;
