@@ -198,7 +198,8 @@ li_status latent_mma(li_ctx* c, const li_paged_cache* cache, const void* q, int 
   a.out = out;
   a.lse = lse;
   a.status = at<int>(ws, 0);
-  a.part_ml = at<float>(ws, kAttnHeader);
+  a.cuts = at<int4>(ws, kAttnHeader);
+  a.part_ml = at<float>(ws, kAttnHeader + up256(static_cast<size_t>(c->num_sms) * sizeof(int4)));
   a.part_o = a.part_ml + static_cast<size_t>(c->num_sms) * 2 * 64 * 2;
   a.part_stride = latent_part_stride(d_v);
   a.wait_ns = c->wait_ns;
@@ -215,9 +216,10 @@ li_status latent_mma(li_ctx* c, const li_paged_cache* cache, const void* q, int 
   a.max_pages = cache->max_pages;
   // whole boxes of rows where a page holds them (the 128-byte swizzle repeats every 8 rows); selected rows come
   // one by one
-  a.box = sel ? 0 : 32;
+  a.box = sel ? 0 : 64;
   while (a.box && cache->page_size % a.box) a.box /= 2;
   if (a.box < 8) a.box = 0;
+  while ((1 << a.box_shift) < a.box) ++a.box_shift;
   if (!latent_mma_layout(&a, c->num_sms, c->max_smem_optin))
     return fail(c, LI_ERR_UNSUPPORTED, "%s: operands too large for shared memory (dim %d)", what, a.dim);
   const cuuint64_t row_bytes = static_cast<cuuint64_t>(a.dim) * 2;
@@ -234,13 +236,13 @@ li_status latent_mma(li_ctx* c, const li_paged_cache* cache, const void* q, int 
   }
   (void)cudaGetLastError();
   {
-    Launch L(c, st, "latent_attn", a.grid, 416, static_cast<int>(a.smem_bytes));
+    Launch L(c, st, "latent_attn", a.grid, 448, static_cast<int>(a.smem_bytes));
     const cudaError_t e = launch_latent_mma(a, st);
     L.done();
     if (e != cudaSuccess) return cuda_fail(c, e, "latent attention launch");
   }
-  if (a.grid == 1) return LI_OK;
-  Launch L(c, st, "latent_join", a.grid - 1, 128, 0);
+  if (a.n_cuts == 0) return LI_OK;
+  Launch L(c, st, "latent_join", a.n_cuts, 128, 0);
   const cudaError_t e = launch_latent_join(a, st);
   L.done();
   return e == cudaSuccess ? LI_OK : cuda_fail(c, e, "latent attention join launch");
@@ -398,7 +400,7 @@ extern "C" {
 
 size_t li_attention_workspace_bytes(const li_ctx* c, int H, int d_v) {
   if (!c || H < 1 || d_v < 1 || d_v > 512) return 0;
-  return kAttnHeader + latent_part_bytes(c->num_sms, d_v);
+  return kAttnHeader + up256(static_cast<size_t>(c->num_sms) * sizeof(int4)) + latent_part_bytes(c->num_sms, d_v);
 }
 
 li_status li_norm_rope(li_ctx* c, const li_head_rows* sets, int n_sets, li_dtype dtype, int64_t n_tok, const int32_t* pos,

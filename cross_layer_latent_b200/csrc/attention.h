@@ -70,6 +70,7 @@ struct alignas(64) LatentMmaArgs {
   float* lse;
   float* part_o;          // [2 grid][64][part_stride] sums of the parts, and
   float* part_ml;         // [2 grid][64][2] their maxima (log2) and weight sums
+  int4* cuts;             // [n_cuts] groups that several CTAs work on: first row, rows (0: none), first and last CTA
   int* status;
   uint64_t wait_ns;
   float scale_log2;       // scale * log2(e)
@@ -78,13 +79,15 @@ struct alignas(64) LatentMmaArgs {
   int T, H, k, dim, d_v;
   int n_pages, page_size, max_pages;
   int box;                // rows of a box (a divisor of the page size), 0: rows one by one always
+  int box_shift;          // log2 of box
   // filled by latent_mma_layout
   int N, groups;          // MMA columns, groups of N rows in a unit
   int nb, last_ksteps;    // 64-column blocks of a row, 16-element K steps of the last one
   int m_blocks;           // blocks of 128 values
-  int slots, bufs;        // 16 KB slots of a tile, tiles held in shared memory
+  int slots, bufs;        // 8 KB slots of a tile, tiles held in shared memory
   int s_bufs;             // score buffers in tensor memory
   int part_stride;
+  int n_cuts, cuts_by_group;
   int grid;
   uint32_t tmem_cols, smem_bytes;
 };

@@ -8,26 +8,50 @@
 
 namespace li {
 
-// Shared-memory matrix descriptor of a 128-byte-swizzled operand with byte
-// offsets between its atoms.  K-major: an atom is 8 rows of 64 bf16, `sbo`
-// apart along the rows (lbo unused).  MN-major: an atom is 8 rows of K, each
-// 64 bf16 along MN; `sbo` steps along K, `lbo` to the next 64 along MN.
-__device__ __forceinline__ uint64_t desc_sw128(uint32_t saddr, uint32_t lbo, uint32_t sbo) {
-  return static_cast<uint64_t>((saddr >> 4) & 0x3FFFu) | (static_cast<uint64_t>((lbo >> 4) & 0x3FFFu) << 16) |
-         (static_cast<uint64_t>((sbo >> 4) & 0x3FFFu) << 32) | (1ull << 46) | (2ull << 61);
-}
-
+// Shared-memory operands are 128-byte swizzled, in two orders.  K-major: an
+// atom is 8 rows of 64 bf16, 1024 bytes (sbo) apart along the rows, lbo
+// unused.  MN-major: an atom is 8 rows of K, each 64 bf16 along MN; 1024 bytes
+// (sbo) step along K, `lbo` bytes to the next 64 along MN.
 // Instruction descriptor bits of operands stored with MN contiguous.
 constexpr uint32_t kMajorMnA = 1u << 15, kMajorMnB = 1u << 16;
 
-// A from tensor memory (bf16 pairs packed in 32-bit columns), B from shared.
-__device__ __forceinline__ void umma_ts_bf16(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
-                                             uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
-      : "memory");
+// Descriptor words of a 128-byte-swizzled operand: the low word holds the
+// address (in 16-byte units) and lbo, the high word the rest, which is the
+// same for every tile.  Steps within a tile add to the low word alone, which
+// keeps the issuing thread's work per MMA to a few instructions.
+__device__ __forceinline__ uint32_t desc_lo(uint32_t saddr, uint32_t lbo) {
+  return ((saddr >> 4) & 0x3FFFu) | (((lbo >> 4) & 0x3FFFu) << 16);
+}
+constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);   // sbo 1024, version 1, 128-byte swizzle
+
+// D += A B over STEPS steps of 16 along K, both operands in shared memory;
+// a_step and b_step are the steps of the low words.  The first step of all
+// overwrites D where `accumulate` is 0.
+template <int STEPS, int A_STEP, int B_STEP>
+__device__ __forceinline__ void umma_ss_steps(uint32_t d_tmem, uint32_t a_lo, uint32_t b_lo, uint32_t idesc, uint32_t accumulate) {
+#pragma unroll
+  for (int k = 0; k < STEPS; ++k) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\t"
+        "mov.b64 a, {%1, %5};\n\tmov.b64 b, {%2, %5};\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_lo + k * A_STEP), "r"(b_lo + k * B_STEP), "r"(idesc), "r"(k == 0 ? accumulate : 1u), "n"(kDescHi)
+        : "memory");
+  }
+}
+
+// The same with A in tensor memory (8 columns of packed pairs a step).
+template <int STEPS, int B_STEP>
+__device__ __forceinline__ void umma_ts_steps(uint32_t d_tmem, uint32_t a_tmem, uint32_t b_lo, uint32_t idesc, uint32_t accumulate) {
+#pragma unroll
+  for (int k = 0; k < STEPS; ++k) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b64 b;\n\t"
+        "mov.b64 b, {%2, %5};\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %3, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_tmem + k * 8), "r"(b_lo + k * B_STEP), "r"(idesc), "r"(k == 0 ? accumulate : 1u), "n"(kDescHi)
+        : "memory");
+  }
 }
 
 // One lane of a converged warp.

@@ -1,16 +1,20 @@
 // latent_mma.cu -- latent attention in absorbed form on the tensor cores.
 //
 // For a group of up to N = 64 query rows of one sequence (heads, and without a
-// selection also neighbouring queries) and 128 cached rows C a tile:
-//     S^T = C Q^T          [128 tokens x N]   A = C (K-major),   B = Q
-//     P^T = exp2(S^T - m)                     one token a thread
+// selection also neighbouring queries) and 64 cached rows C a tile:
+//     S^T = C Q^T          [64 tokens x N]    A = C (K-major),   B = Q
+//     P^T = exp2(S^T - m)
 //     O^T += C[:, :d_v]^T P^T [d_v x N]       A = C (MN-major),  B = P^T
-// Tokens lie along the MMA's M, so the N dimension and the work shrink with
+// Tokens lie along the scores' M, so the N dimension and the work shrink with
 // the head count (16, 32 or 64), the same tile in shared memory serves as key
 // and as value, and O^T takes 4 N <= 256 tensor-memory columns, which leaves
-// room for S^T.  (Heads along M would put 512 columns of output next to the
-// scores, more than there are.)  Cost: at N = 64 an MMA is bound by its 6 KB of
-// shared-memory operands, 48 cycles instead of 32.
+// room for two S^T.  (Heads along M would put 512 columns of output next to
+// the scores, more than there are.)  The tile is 64 tokens because two then
+// fit next to the queries (2 x 72 KB + 72 KB at 576 x 64): one is loaded while
+// the other is worked on.  With one tile of 128 tokens the loads waited for
+// the products and the products for the loads: 10,200 cycles a tile of 128
+// against 5,000 of MMA, 189 us for 4 x 131072 rows.  Cost of the small tile:
+// the scores' MMAs run at M = 64, 32 cycles for half the tokens (48 at M = 128).
 //
 // The running maximum m is kept per head and moves only when a score exceeds
 // it by more than 8 (in powers of two): then weights stay below 256 and
@@ -18,7 +22,7 @@
 // the common tile needs no reduction over the tokens, which lie across lanes.
 // The sums of the weights are taken before they are rounded to bf16.
 //
-// P^T (128 tokens x N) overwrites the tile's last 64-column block, which holds
+// P^T (64 tokens x N) overwrites the tile's last 64-column block, which holds
 // rotary columns only and is no longer needed once S^T is complete; where
 // the last block belongs to the values, a spare block is set aside.
 //
@@ -35,31 +39,35 @@ namespace li {
 
 namespace {
 
-constexpr int kTile = 128;                       // tokens per tile
-constexpr int kBlockBytes = kTile * 128;         // 128 tokens x 64 bf16
+constexpr int kTile = 64;                        // tokens per tile
+constexpr int kBlockBytes = kTile * 128;         // 64 tokens x 64 bf16
 constexpr int kSoftWarps = 8;                    // two warpgroups, half of the N columns each
 constexpr int kMmaWarp = kSoftWarps;
-constexpr int kLoadWarps = 4;                    // 32 tokens of a tile each
-constexpr int kThreads = 32 * (kSoftWarps + 1 + kLoadWarps);
+constexpr int kLookWarp = kMmaWarp + 1;           // finds the pool rows of tiles ahead
+constexpr int kLoadWarps = 4;
+constexpr int kLook = 4;                         // tiles that it may be ahead (a power of two)
+constexpr int kHalf = 4;                         // blocks of a tile's first part; the rest is the second
+constexpr int kThreads = 32 * (kSoftWarps + 2 + kLoadWarps);
 constexpr int kMaxBufs = 4;
-constexpr int kMaxBlocks = 10;
+constexpr int kMaxSlots = 9;
 constexpr float kGrow = 8.f;                     // log2 by which a score may exceed the kept maximum
 constexpr float kNoMax = -1e30f;
 constexpr uint64_t kDrainNs = 1000ull * 1000ull;
 
 struct Smem {
-  uint64_t full[kMaxBufs][kMaxBlocks / 2];       // two blocks (a pair) arrived
-  uint64_t empty[kMaxBufs][kMaxBlocks / 2];      // they are free again
-  uint64_t meta[kMaxBufs];                       // tokens' valid bits written
+  uint64_t full[kMaxBufs][2];                    // part of a tile arrived
+  uint64_t empty[kMaxBufs][2];                   // it is free again
+  uint64_t look_full[kLook], look_empty[kLook];  // pool rows of a tile's tokens
   uint64_t q_full, q_empty, s_full[2], p_full[2], pv_done, o_full, o_empty, drain;
   uint32_t tmem;
   int abort_flag;
   int first_b, first_g, first_tile;
   int64_t total;
-  uint32_t valid[kMaxBufs][4];
+  alignas(8) uint32_t valid[kLook][2];           // tokens that are there
+  alignas(16) int row[kLook][kTile];             // their pool rows, -1: nobody attends the token
   alignas(16) float m[64];
   alignas(16) float alpha[64];
-  float part[4][64];
+  alignas(16) float part[4][64];
   int limit[64];
 };
 
@@ -191,6 +199,32 @@ __device__ __forceinline__ void cp_async_16_or_zero(uint32_t dst, const void* sr
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(src_bytes) : "memory");
 }
 
+// Reads a 64-row accumulator: 16 lanes x 8 K columns, rows lane / 4 and
+// lane / 4 + 8, columns 8 i + 2 (lane % 4) + {0, 1} in r[4 i ...].
+template <int K>
+__device__ __forceinline__ void tmem_ld_rows16(uint32_t taddr, uint32_t (&r)[4 * K]) {
+  static_assert(K == 1 || K == 2 || K == 4, "8, 16 or 32 columns");
+  if constexpr (K == 1) {
+    asm volatile("tcgen05.ld.sync.aligned.16x256b.x1.b32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(taddr)
+                 : "memory");
+  } else if constexpr (K == 2) {
+    asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                 : "r"(taddr)
+                 : "memory");
+  } else {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr)
+        : "memory");
+  }
+}
+
 template <int N>
 __global__ void __launch_bounds__(kThreads, 1) latent_mma_kernel(const __grid_constant__ LatentMmaArgs a) {
   extern __shared__ uint8_t raw[];
@@ -200,16 +234,19 @@ __global__ void __launch_bounds__(kThreads, 1) latent_mma_kernel(const __grid_co
   const uint32_t tiles_smem = q_smem + a.nb * N * 128;
   Smem& sm = *reinterpret_cast<Smem*>(base + a.nb * N * 128 + static_cast<size_t>(a.bufs) * a.slots * kBlockBytes);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int pairs = (a.slots + 1) / 2;
+  const int parts = a.slots > kHalf ? 2 : 1;
   const WaitCtl wc{&sm.abort_flag, a.status, a.wait_ns};
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < a.bufs; ++i) {
-      for (int j = 0; j < pairs; ++j) {
+      for (int j = 0; j < parts; ++j) {
         mbar_init(&sm.full[i][j], 32 * kLoadWarps);
         mbar_init(&sm.empty[i][j], 1);
       }
-      mbar_init(&sm.meta[i], kLoadWarps);
+    }
+    for (int i = 0; i < kLook; ++i) {
+      mbar_init(&sm.look_full[i], 1);
+      mbar_init(&sm.look_empty[i], kSoftWarps + kLoadWarps);
     }
     mbar_init(&sm.q_full, 1);
     mbar_init(&sm.q_empty, 1);
@@ -245,6 +282,7 @@ __global__ void __launch_bounds__(kThreads, 1) latent_mma_kernel(const __grid_co
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  pdl_release();
   const uint32_t tmem = sm.tmem;
   const uint32_t o_tmem = tmem, s_tmem = tmem + a.m_blocks * N;
 
@@ -253,6 +291,10 @@ __global__ void __launch_bounds__(kThreads, 1) latent_mma_kernel(const __grid_co
     const int wg = warp >> 2, quad = warp & 3;
     const uint32_t lanes = static_cast<uint32_t>(quad * 32) << 16;
     const int c0 = wg * CW;                      // first column
+    constexpr int K = CW / 8;
+    // M = 64 accumulators lie in 16 lanes of each quarter; read in 16-lane rows a thread has tokens tok and
+    // tok + 8 and of every eight columns two
+    const int tok = quad * 16 + (lane >> 2), cl = (lane & 3) * 2;
     const int bar = 1 + wg;
     Walk w;
     Ring ring, sring;                            // tile buffers, score buffers
@@ -269,53 +311,65 @@ __global__ void __launch_bounds__(kThreads, 1) latent_mma_kernel(const __grid_co
         if (column_limits) sm.limit[c] = c < rows ? row_limit(a, w.s.b, r0 + c, n) : 0;
       }
       named_bar_sync(bar, 128);
-      float sum[CW];
+      float sum[K][2];                           // of this thread's two rows, by column
 #pragma unroll
-      for (int i = 0; i < CW; ++i) sum[i] = 0.f;
+      for (int i = 0; i < K; ++i) sum[i][0] = sum[i][1] = 0.f;
       for (int t = w.s.t0; t < w.s.t1; ++t, ++tile) {
         const int buf = ring.buf, sb = sring.buf;
-        bool ok = bounded_wait(&sm.meta[buf], ring.ph, wc);
+        const int lk = tile % kLook;
+        bool ok = bounded_wait(&sm.look_full[lk], (tile / kLook) & 1u, wc);
         ok = bounded_wait(&sm.s_full[sb], sring.ph, wc) && ok;
         ring.step(a.bufs);
         sring.step(a.s_bufs);
         __syncwarp();
         tc_fence_after();
-        uint32_t xr[CW];
-        tmem_ld<CW>(s_tmem + sb * N + c0 + lanes, xr);
-        const bool live = (sm.valid[buf][quad] >> lane) & 1u;
+        uint32_t xr[4 * K];
+        tmem_ld_rows16<K>(s_tmem + sb * N + c0 + lanes, xr);
+        const uint64_t valid = *reinterpret_cast<const uint64_t*>(sm.valid[lk]) >> tok;
+        const bool live[2] = {(valid & 1u) != 0, (valid >> 8 & 1u) != 0};
         tmem_wait_ld();
-        float x[CW];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.look_empty[lk]);
+        // x[i][e]: token tok + 8 (e / 2), column c0 + 8 i + cl + e % 2
+        float x[K][4];
 #pragma unroll
-        for (int i = 0; i < CW; ++i) x[i] = live ? __uint_as_float(xr[i]) * a.scale_log2 : -INFINITY;
+        for (int i = 0; i < K; ++i)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) x[i][e] = live[e >> 1] ? __uint_as_float(xr[4 * i + e]) * a.scale_log2 : -INFINITY;
         if (column_limits) {
-          const int s = t * kTile + quad * 32 + lane;
+          const int at = t * kTile + tok;
 #pragma unroll
-          for (int i = 0; i < CW; ++i)
-            if (s >= sm.limit[c0 + i]) x[i] = -INFINITY;
+          for (int i = 0; i < K; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              if (at + 8 * (e >> 1) >= sm.limit[c0 + 8 * i + cl + (e & 1)]) x[i][e] = -INFINITY;
         }
         bool grow = t == w.s.t0;
         if (!grow) {
           float over = -INFINITY;
 #pragma unroll
-          for (int i = 0; i < CW; i += 4) {
-            const float4 m = *reinterpret_cast<const float4*>(&sm.m[c0 + i]);
-            over = fmaxf(over, fmaxf(fmaxf(x[i] - m.x, x[i + 1] - m.y), fmaxf(x[i + 2] - m.z, x[i + 3] - m.w)));
+          for (int i = 0; i < K; ++i) {
+            const float2 m = *reinterpret_cast<const float2*>(&sm.m[c0 + 8 * i + cl]);
+            over = fmaxf(over, fmaxf(fmaxf(x[i][0], x[i][2]) - m.x, fmaxf(x[i][1], x[i][3]) - m.y));
           }
           grow = named_bar_any(bar, 128, over > kGrow || !ok);
         }
         if (grow) {
-          // new maxima over the tile's 128 tokens, and what they make of the old sums
+          // new maxima over the tile's tokens, and what they make of the old sums
           if (named_bar_any(bar, 128, !ok)) {
             dead = true;
             break;
           }
-          float top = 0.f;
 #pragma unroll
-          for (int i = 0; i < CW; ++i) {
-            const float r = warp_max_f32(x[i]);
-            if (lane == i) top = r;
+          for (int i = 0; i < K; ++i) {
+            float2 top = make_float2(fmaxf(x[i][0], x[i][2]), fmaxf(x[i][1], x[i][3]));
+#pragma unroll
+            for (int o = 4; o < 32; o <<= 1) {
+              top.x = fmaxf(top.x, __shfl_xor_sync(0xffffffffu, top.x, o));
+              top.y = fmaxf(top.y, __shfl_xor_sync(0xffffffffu, top.y, o));
+            }
+            if (lane < 4) *reinterpret_cast<float2*>(&sm.part[quad][c0 + 8 * i + cl]) = top;
           }
-          if (lane < CW) sm.part[quad][c0 + lane] = top;
           named_bar_sync(bar, 128);
           if (threadIdx.x % 128 < CW) {
             const int c = c0 + threadIdx.x % 128;
@@ -333,12 +387,10 @@ __global__ void __launch_bounds__(kThreads, 1) latent_mma_kernel(const __grid_co
             }
             tc_fence_after();
 #pragma unroll
-            for (int i = 0; i < CW; i += 4) {
-              const float4 f = *reinterpret_cast<const float4*>(&sm.alpha[c0 + i]);
-              sum[i] *= f.x;
-              sum[i + 1] *= f.y;
-              sum[i + 2] *= f.z;
-              sum[i + 3] *= f.w;
+            for (int i = 0; i < K; ++i) {
+              const float2 f = *reinterpret_cast<const float2*>(&sm.alpha[c0 + 8 * i + cl]);
+              sum[i][0] *= f.x;
+              sum[i][1] *= f.y;
             }
             constexpr int R = CW < 16 ? CW : 16;   // columns in registers at a time
             for (int u = 0; u < a.m_blocks * (CW / R); ++u) {
@@ -360,22 +412,18 @@ __global__ void __launch_bounds__(kThreads, 1) latent_mma_kernel(const __grid_co
             tmem_wait_st();
           }
         }
-        // weights, their sums, and P^T: token = row of 128 bytes, heads along it
-        const uint32_t p_row = tiles_smem + (buf * a.slots + a.slots - 1) * kBlockBytes + (quad * 32 + lane) * 128;
+        // weights, their sums, and P^T: a token is a row of 128 bytes, heads along it
+        const uint32_t p_row = tiles_smem + (buf * a.slots + a.slots - 1) * kBlockBytes + tok * 128 + cl * 2;
 #pragma unroll
-        for (int i = 0; i < CW; i += 8) {
-          float p[8], m[8];
-          *reinterpret_cast<float4*>(&m[0]) = *reinterpret_cast<const float4*>(&sm.m[c0 + i]);
-          *reinterpret_cast<float4*>(&m[4]) = *reinterpret_cast<const float4*>(&sm.m[c0 + i + 4]);
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            p[e] = exp2_fast(x[i + e] - m[e]);
-            sum[i + e] += p[e];
-          }
-          const uint32_t chunk = static_cast<uint32_t>((c0 + i) / 8) ^ static_cast<uint32_t>(lane & 7);
-          asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(p_row + chunk * 16), "r"(pack_bf16(p[0], p[1])),
-                       "r"(pack_bf16(p[2], p[3])), "r"(pack_bf16(p[4], p[5])), "r"(pack_bf16(p[6], p[7]))
-                       : "memory");
+        for (int i = 0; i < K; ++i) {
+          const float2 m = *reinterpret_cast<const float2*>(&sm.m[c0 + 8 * i + cl]);
+          const float p0 = exp2_fast(x[i][0] - m.x), p1 = exp2_fast(x[i][1] - m.y);
+          const float p2 = exp2_fast(x[i][2] - m.x), p3 = exp2_fast(x[i][3] - m.y);
+          sum[i][0] += p0 + p2;
+          sum[i][1] += p1 + p3;
+          const uint32_t at = p_row + (static_cast<uint32_t>((c0 / 8 + i) ^ (lane >> 2)) << 4);
+          asm volatile("st.shared.b32 [%0], %1;" ::"r"(at), "r"(pack_bf16(p0, p1)) : "memory");
+          asm volatile("st.shared.b32 [%0], %1;" ::"r"(at + 8 * 128), "r"(pack_bf16(p2, p3)) : "memory");
         }
         fence_proxy_async_smem();
         tc_fence_before();
@@ -385,14 +433,16 @@ __global__ void __launch_bounds__(kThreads, 1) latent_mma_kernel(const __grid_co
       if (dead) break;
       // ---- sums over the tokens
 #pragma unroll
-      for (int i = 0; i < CW; ++i) {
+      for (int i = 0; i < K; ++i)
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) sum[i] += __shfl_xor_sync(0xffffffffu, sum[i], o);
-      }
+        for (int o = 4; o < 32; o <<= 1) {
+          sum[i][0] += __shfl_xor_sync(0xffffffffu, sum[i][0], o);
+          sum[i][1] += __shfl_xor_sync(0xffffffffu, sum[i][1], o);
+        }
       named_bar_sync(bar, 128);                  // the last maxima have been read
-      if (lane == 0) {
+      if (lane < 4) {
 #pragma unroll
-        for (int i = 0; i < CW; ++i) sm.part[quad][c0 + i] = sum[i];
+        for (int i = 0; i < K; ++i) *reinterpret_cast<float2*>(&sm.part[quad][c0 + 8 * i + cl]) = make_float2(sum[i][0], sum[i][1]);
       }
       named_bar_sync(bar, 128);
       const bool whole = w.s.t0 == 0 && w.s.t1 == w.s.tiles;
@@ -441,65 +491,71 @@ __global__ void __launch_bounds__(kThreads, 1) latent_mma_kernel(const __grid_co
   } else if (warp == kMmaWarp) {
     // ------------------------------------------------ MMA issue, one lane
     if (elect_one()) {
-      const uint32_t id_s = make_instr_desc(1, 128, N);
-      const uint32_t id_o = id_s | kMajorMnA | kMajorMnB;
+      const uint32_t id_s = make_instr_desc(1, 64, N);
+      const uint32_t id_o = make_instr_desc(1, 128, N) | kMajorMnA | kMajorMnB;
       Walk w;
       Ring sr, ssr, vr, vsr;                     // tile and score buffers of the next scores, of the next values
       uint32_t seg = 0;
       bool ok = true;
-      const uint64_t da0 = desc_sw128(tiles_smem, 16, 1024), db0 = desc_sw128(q_smem, 16, 1024);
-      const uint64_t dv0 = desc_sw128(tiles_smem, kBlockBytes, 1024);
-      constexpr uint64_t kBlockDesc = kBlockBytes >> 4, kQDesc = (N * 128) >> 4;
-      // S^T of the next tile
-      auto scores = [&]() {
+      const uint32_t c0 = desc_lo(tiles_smem, 0), q0 = desc_lo(q_smem, 0), v0 = desc_lo(tiles_smem, kBlockBytes);
+      constexpr uint32_t kBlockStep = kBlockBytes >> 4, kQStep = (N * 128) >> 4;
+      const uint32_t tile_step = a.slots * kBlockStep;
+      // S^T of the next tile, part p
+      auto scores = [&](int p) {
+        if (!bounded_wait(&sm.full[sr.buf][p], sr.ph, wc)) return false;
+        fence_proxy_async_smem();                // rows gathered by cp.async are read by the tensor cores
+        tc_fence_after();
         const uint32_t d = s_tmem + ssr.buf * N;
-        uint64_t da = da0 + sr.buf * a.slots * kBlockDesc, db = db0;
-        uint32_t acc = 0;
-        for (int p = 0; p < pairs; ++p) {
-          const int nblk = min(2, a.nb - 2 * p);
-          if (nblk <= 0) break;
-          if (!bounded_wait(&sm.full[sr.buf][p], sr.ph, wc)) return false;
-          fence_proxy_async_smem();              // rows gathered by cp.async are read by the tensor cores
-          tc_fence_after();
-          for (int j = 0; j < nblk; ++j, da += kBlockDesc, db += kQDesc) {
-            const int ks = 2 * p + j == a.nb - 1 ? a.last_ksteps : 4;
-#pragma unroll
-            for (int kk = 0; kk < 4; ++kk) {
-              if (kk < ks) umma<kKindBF16>(d, da + 2 * kk, db + 2 * kk, id_s, acc);
-              acc = 1;
-            }
+        const int end = p == 0 ? min(kHalf, a.nb) : a.nb;
+        uint32_t c = c0 + sr.buf * tile_step + p * kHalf * kBlockStep, q = q0 + p * kHalf * kQStep;
+        for (int j = p * kHalf; j < end; ++j, c += kBlockStep, q += kQStep) {
+          if (j < a.nb - 1 || a.last_ksteps == 4) {
+            umma_ss_steps<4, 2, 2>(d, c, q, id_s, j > 0 ? 1u : 0u);
+          } else {
+            for (int k = 0; k < a.last_ksteps; ++k) umma_ss_steps<1, 2, 2>(d, c + 2 * k, q + 2 * k, id_s, j + k > 0 ? 1u : 0u);
           }
         }
-        umma_commit(&sm.s_full[ssr.buf]);
-        sr.step(a.bufs);
-        ssr.step(a.s_bufs);
+        if (p == parts - 1) {
+          umma_commit(&sm.s_full[ssr.buf]);
+          sr.step(a.bufs);
+          ssr.step(a.s_bufs);
+        }
         return true;
       };
       for (bool more = w.start(a, sm); more && ok; more = w.next(a), ++seg) {
         if (!(ok = bounded_wait(&sm.q_full, seg & 1u, wc))) break;
         const int nt = w.s.t1 - w.s.t0;
-        const int ahead = a.s_bufs - 1;          // scores run one tile ahead where there are two buffers
-        int issued = 0;
-        for (int t = 0; t < nt && ok; ++t) {
-          while (ok && issued < nt && issued <= t + ahead) {
-            ok = scores();
+        int issued = 0, part = 0;                // tiles whose scores are issued, parts of the next one
+        auto next_scores = [&]() {
+          ok = scores(part);
+          if (++part == parts) {
+            part = 0;
             if (++issued == nt) umma_commit(&sm.q_empty);
+          }
+        };
+        for (int t = 0; t < nt && ok; ++t) {
+          while (ok && issued == t) next_scores();
+          if (!ok) break;
+          // the next tile's scores go first, part by part, as far as that tile is here before this one's weights are
+          if (a.s_bufs == 2 && issued < nt) {
+            const uint64_t began = cycles();
+            while (ok && issued == t + 1 && issued < nt && !mbar_test_wait(&sm.p_full[vsr.buf], vsr.ph)) {
+              if (mbar_test_wait(&sm.full[sr.buf][part], sr.ph)) next_scores();
+              else if (*wc.abort_flag || cycles() - began > a.wait_ns * kCyclesPerNs) ok = give_up(wc);
+            }
           }
           if (!ok) break;
           if (t == 0 && seg > 0 && !(ok = bounded_wait(&sm.o_empty, (seg - 1) & 1u, wc))) break;
           if (!(ok = bounded_wait(&sm.p_full[vsr.buf], vsr.ph, wc))) break;
           tc_fence_after();
-          const uint64_t dt = dv0 + vr.buf * a.slots * kBlockDesc;
-          const uint64_t dp = dt + (a.slots - 1) * kBlockDesc;
+          const uint32_t v = v0 + vr.buf * tile_step, pt = v + (a.slots - 1) * kBlockStep;
           uint64_t* const empty = sm.empty[vr.buf];
           for (int mb = 0; mb < a.m_blocks; ++mb) {
-            const uint64_t dv = dt + 2 * mb * kBlockDesc;
-#pragma unroll
-            for (int kk = 0; kk < 8; ++kk)
-              umma<kKindBF16>(o_tmem + mb * N, dv + kk * 128, dp + kk * 128, id_o, (t > 0 || kk > 0) ? 1u : 0u);
-            if (mb < a.m_blocks - 1) umma_commit(&empty[mb]);
+            umma_ss_steps<kTile / 16, 128, 128>(o_tmem + mb * N, v + 2 * mb * kBlockStep, pt, id_o, t > 0 ? 1u : 0u);
+            if (2 * (mb + 1) == kHalf && parts == 2 && mb < a.m_blocks - 1) umma_commit(&empty[0]);
           }
-          for (int p = a.m_blocks - 1; p < pairs; ++p) umma_commit(&empty[p]);
+          if (parts == 1 || 2 * a.m_blocks <= kHalf) umma_commit(&empty[0]);
+          if (parts == 2) umma_commit(&empty[1]);
           umma_commit(&sm.pv_done);
           if (t == nt - 1) umma_commit(&sm.o_full);
           vr.step(a.bufs);
@@ -511,27 +567,26 @@ __global__ void __launch_bounds__(kThreads, 1) latent_mma_kernel(const __grid_co
       drain_wait(&sm.drain, 0, kDrainNs);
     }
     __syncwarp();
-  } else {
-    // ------------------------------------------------ loads
-    const int lw = warp - kMmaWarp - 1;          // 32 tokens of every tile
+  } else if (warp == kLookWarp) {
+    // ------------------------------------------------ pool rows of the tiles
     Walk w;
-    Ring ring;
-    uint32_t seg = 0, queries = 0;
-    int64_t tile = 0;
+    uint32_t tile = 0;
     bool ok = true;
-    const uint32_t my_rows = tiles_smem + lw * 32 * 128;
-    for (bool more = w.start(a, sm); more && ok; more = w.next(a), ++seg) {
-      // queries of the group (one lane), once the previous group's scores are done
-      if (lw == 0) {
-        if (seg > 0) ok = __all_sync(0xffffffffu, bounded_wait(&sm.q_empty, (seg - 1) & 1u, wc));
-        if (!ok) break;
-        if (lane == 0) {
-          mbar_arrive_expect_tx(&sm.q_full, a.nb * N * 128);
-          for (int j = 0; j < a.nb; ++j)
-            tma_load_3d(base + j * N * 128, &a.map_q, &sm.q_full, 64 * j, w.s.g * N, w.s.b);
+    // the CTAs behind this one that work on its last group, for the join
+    if (!a.cuts_by_group && lane == 0 && static_cast<int>(blockIdx.x) < a.n_cuts) a.cuts[blockIdx.x] = make_int4(0, 0, 0, 0);
+    for (bool more = w.start(a, sm); more && ok; more = w.next(a)) {
+      if (lane == 0 && w.s.t0 == 0 && a.n_cuts > 0) {
+        const int64_t group = static_cast<int64_t>(w.s.b) * a.groups + w.s.g;
+        const bool cut = w.s.t1 < w.s.tiles;
+        int4 c = make_int4(0, 0, 0, 0);
+        if (cut) {
+          // the share that holds tile x is the largest i with total * i / n <= x
+          const int64_t n = shares(a, sm.total), last = sm.total * (blockIdx.x + 1) / n - w.s.t1 + w.s.tiles - 1;
+          c = make_int4(static_cast<int>(w.s.b * static_cast<int64_t>(a.rows) + w.s.g * N), min(N, a.rows - w.s.g * N), blockIdx.x,
+                        static_cast<int>(((last + 1) * n - 1) / sm.total));
         }
-        ++queries;
-        __syncwarp();
+        if (a.cuts_by_group) a.cuts[group] = c;
+        else if (cut) a.cuts[blockIdx.x] = c;
       }
       // what the group's rows see at most; positions and pages of a tile are read two and one tiles ahead
       const int seq = a.sel ? w.s.b / a.T : w.s.b;
@@ -545,8 +600,9 @@ __global__ void __launch_bounds__(kThreads, 1) latent_mma_kernel(const __grid_co
       }
       const int32_t* table = a.page_table + static_cast<int64_t>(seq) * a.max_pages;
       const int32_t* sel = a.sel ? a.sel + static_cast<int64_t>(w.s.b) * a.k : nullptr;
-      auto position = [&](int t) {               // of this lane's token in tile t; -1: none
-        const int64_t i = static_cast<int64_t>(t) * kTile + lw * 32 + lane;
+      // a lane looks after tokens lane and lane + 32 of a tile
+      auto position = [&](int t, int half) {     // -1: none
+        const int64_t i = static_cast<int64_t>(t) * kTile + half * 32 + lane;
         if (t >= w.s.t1) return -1;
         if (!sel) return i < lim ? static_cast<int>(i) : -1;
         return i < a.k ? sel[i] : -1;
@@ -560,78 +616,117 @@ __global__ void __launch_bounds__(kThreads, 1) latent_mma_kernel(const __grid_co
         return s < 0 ? -1 : s;
       };
       auto page_of = [&](int s) { return s >= 0 ? table[s / a.page_size] : 0; };
-      int s0 = checked(position(w.s.t0));
-      int pg0 = page_of(s0);
-      int s1 = position(w.s.t0 + 1);
+      int s0[2], pg[2], s1[2];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        s0[h] = checked(position(w.s.t0, h));
+        s1[h] = position(w.s.t0 + 1, h);
+      }
+#pragma unroll
+      for (int h = 0; h < 2; ++h) pg[h] = page_of(s0[h]);
+      for (int t = w.s.t0; t < w.s.t1; ++t, ++tile) {
+        const int lk = tile % kLook;
+        int row[2];
+        unsigned valid[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          if (s0[h] >= 0 && (pg[h] < 0 || pg[h] >= a.n_pages)) {
+            record_status(a.status, kStatusIndex);
+            s0[h] = -1;
+          }
+          row[h] = s0[h] >= 0 ? pg[h] * a.page_size + s0[h] % a.page_size : -1;
+          valid[h] = __ballot_sync(0xffffffffu, s0[h] >= 0);
+          // next tile's pages, and the positions after that
+          s0[h] = checked(s1[h]);
+          pg[h] = page_of(s0[h]);
+          s1[h] = position(t + 2, h);
+        }
+        if (tile >= kLook) ok = __all_sync(0xffffffffu, bounded_wait(&sm.look_empty[lk], (tile / kLook - 1) & 1u, wc));
+        if (!ok) break;
+        sm.row[lk][lane] = row[0];
+        sm.row[lk][lane + 32] = row[1];
+        if (lane == 0) {
+          sm.valid[lk][0] = valid[0];
+          sm.valid[lk][1] = valid[1];
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.look_full[lk]);
+      }
+    }
+  } else {
+    // ------------------------------------------------ loads
+    const int lw = warp - kLookWarp - 1;
+    Walk w;
+    Ring ring;
+    uint32_t seg = 0, queries = 0;
+    int64_t tile = 0;
+    bool ok = true;
+    // a box of rows to a lane, or eight lanes a row, four rows at a time, in 16-byte pieces (rows 16 lw ... of a
+    // tile); 128-byte swizzle: piece c of row r lies at c ^ (r mod 8)
+    const int per = kTile >> a.box_shift, at = (lane & (per - 1)) << a.box_shift;
+    const int c = lane & 7, r4 = lane >> 3;
+    const uint32_t even = (16 * lw + r4) * 128 + ((c ^ r4) << 4), odd = (16 * lw + r4) * 128 + ((c ^ (4 + r4)) << 4);
+    for (bool more = w.start(a, sm); more && ok; more = w.next(a), ++seg) {
+      // queries of the group (one lane), once the previous group's scores are done
+      if (lw == 0) {
+        if (seg > 0) ok = __all_sync(0xffffffffu, bounded_wait(&sm.q_empty, (seg - 1) & 1u, wc));
+        if (!ok) break;
+        if (lane == 0) {
+          mbar_arrive_expect_tx(&sm.q_full, a.nb * N * 128);
+          for (int j = 0; j < a.nb; ++j)
+            tma_load_3d(base + j * N * 128, &a.map_q, &sm.q_full, 64 * j, w.s.g * N, w.s.b);
+        }
+        ++queries;
+        __syncwarp();
+      }
       for (int t = w.s.t0; t < w.s.t1; ++t, ++tile) {
         const int buf = ring.buf;
         const uint32_t free_phase = ring.ph ^ 1u;
         ring.step(a.bufs);
-        if (s0 >= 0 && (pg0 < 0 || pg0 >= a.n_pages)) {
-          record_status(a.status, kStatusIndex);
-          s0 = -1;
-        }
-        const int row = s0 >= 0 ? pg0 * a.page_size + s0 % a.page_size : -1;
-        const unsigned valid = __ballot_sync(0xffffffffu, s0 >= 0);
-        const bool boxes = a.box && valid == 0xffffffffu;
-        // next tile's pages, and the positions after that
-        s0 = checked(s1);
-        pg0 = page_of(s0);
-        s1 = position(t + 2);
-        const uint32_t dst = my_rows + buf * a.slots * kBlockBytes;
-        const bool wait = tile >= a.bufs;
+        const int lk = static_cast<int>(tile & (kLook - 1));
+        ok = __all_sync(0xffffffffu, bounded_wait(&sm.look_full[lk], static_cast<uint32_t>(tile / kLook) & 1u, wc));
+        if (!ok) break;
+        const bool boxes = a.box && (sm.valid[lk][0] & sm.valid[lk][1]) == 0xffffffffu;
+        int box_row = 0;
+        const uint8_t* src[4];
+        uint32_t there = 0;
         if (boxes) {
-          // lane i < 32 / box loads box i of every block
-          const int i = lane & (32 / a.box - 1);
-          const int r = __shfl_sync(0xffffffffu, row, i * a.box);
-          uint8_t* to = base + (dst - q_smem) + i * a.box * 128;
-          for (int p = 0; p < pairs && ok; ++p) {
-            const int nblk = min(2, a.nb - 2 * p);
-            if (wait) ok = __all_sync(0xffffffffu, bounded_wait(&sm.empty[buf][p], free_phase, wc));
-            if (!ok) break;
-            if (lane == 0) {
-              if (p == 0) {
-                sm.valid[buf][lw] = valid;
-                mbar_arrive(&sm.meta[buf]);
-              }
-              if (nblk > 0) {
-                mbar_arrive_n(&sm.full[buf][p], 31);
-                mbar_arrive_expect_tx(&sm.full[buf][p], nblk * 32 * 128);
-              }
-            }
-            if (lane < 32 / a.box)
-              for (int j = 2 * p; j < 2 * p + nblk; ++j) tma_load_2d(to + j * kBlockBytes, &a.map_box, &sm.full[buf][p], 64 * j, r);
-          }
+          box_row = sm.row[lk][at & (kTile - 1)];
         } else {
-          // eight lanes a row, four rows at a time, in 16-byte pieces; tokens that nobody attends become zeros
-          const int c = lane & 7;
-          const uint8_t* src[8];
-          uint32_t there = 0;
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const int r = __shfl_sync(0xffffffffu, row, 4 * i + (lane >> 3));
+          for (int i = 0; i < 4; ++i) {
+            const int r = sm.row[lk][16 * lw + 4 * i + r4];
             if (r >= 0) there |= 1u << i;
             src[i] = static_cast<const uint8_t*>(a.data) + static_cast<int64_t>(max(r, 0)) * a.dim * 2 + c * 16;
           }
-          // 128-byte swizzle: piece c of row r lies at c ^ (r mod 8); rows 4 i + lane / 8
-          const uint32_t even = dst + (lane >> 3) * 128 + ((c ^ (lane >> 3)) << 4);
-          const uint32_t odd = dst + (lane >> 3) * 128 + ((c ^ (4 + (lane >> 3))) << 4);
-          for (int p = 0; p < pairs && ok; ++p) {
-            const int nblk = min(2, a.nb - 2 * p);
-            if (wait) ok = __all_sync(0xffffffffu, bounded_wait(&sm.empty[buf][p], free_phase, wc));
-            if (!ok) break;
-            if (p == 0 && lane == 0) {
-              sm.valid[buf][lw] = valid;
-              mbar_arrive(&sm.meta[buf]);
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.look_empty[lk]);
+        const uint32_t dst = tiles_smem + buf * a.slots * kBlockBytes;
+        for (int p = 0; p < parts; ++p) {
+          const int end = p == 0 ? min(kHalf, a.nb) : a.nb;
+          if (tile >= a.bufs) ok = __all_sync(0xffffffffu, bounded_wait(&sm.empty[buf][p], free_phase, wc));
+          if (!ok) break;
+          if (boxes) {
+            // blocks p * kHalf + lw, + 4, ... are this warp's
+            const int first = p * kHalf + lw;
+            const int mine = first < end ? (end - first + kLoadWarps - 1) / kLoadWarps : 0;
+            if (lane == 0) {
+              mbar_arrive_n(&sm.full[buf][p], 31);
+              mbar_arrive_expect_tx(&sm.full[buf][p], mine * kBlockBytes);
             }
-            if (nblk <= 0) continue;
-            for (int j = 2 * p; j < 2 * p + nblk; ++j) {
+            if (lane < per)
+              for (int j = first; j < end; j += kLoadWarps)
+                tma_load_2d(base + (dst - q_smem) + j * kBlockBytes + at * 128, &a.map_box, &sm.full[buf][p], 64 * j, box_row);
+          } else {
+            for (int j = p * kHalf; j < end; ++j) {
               const bool in_row = 64 * j + c * 8 < a.dim;
 #pragma unroll
-              for (int i = 0; i < 8; ++i) {
+              for (int i = 0; i < 4; ++i) {
+                // tokens that nobody attends, and columns past the row, become zeros
                 const bool on = in_row && ((there >> i) & 1u);
-                cp_async_16_or_zero((i & 1 ? odd : even) + j * kBlockBytes + i * 512, on ? src[i] + j * 128 : static_cast<const uint8_t*>(a.data),
-                                    on ? 16u : 0u);
+                cp_async_16_or_zero(dst + (i & 1 ? odd : even) + j * kBlockBytes + i * 512,
+                                    on ? src[i] + j * 128 : static_cast<const uint8_t*>(a.data), on ? 16u : 0u);
               }
             }
             cp_async_arrive_noinc(&sm.full[buf][p]);
@@ -643,7 +738,7 @@ __global__ void __launch_bounds__(kThreads, 1) latent_mma_kernel(const __grid_co
     // the copies that were issued land before the CTA ends, whichever role gave up
     cp_async_wait_all();
     for (int64_t i = max(tile - a.bufs, int64_t(0)); i < tile; ++i)
-      for (int p = 0; 2 * p < a.nb; ++p)
+      for (int p = 0; p < parts; ++p)
         drain_wait(&sm.full[i % a.bufs][p], static_cast<uint32_t>(i / a.bufs) & 1u, kDrainNs);
     if (lw == 0 && queries > 0) drain_wait(&sm.q_full, (queries - 1) & 1u, kDrainNs);
   }
@@ -653,23 +748,15 @@ __global__ void __launch_bounds__(kThreads, 1) latent_mma_kernel(const __grid_co
   if (warp == kMmaWarp) tmem_dealloc(tmem, a.tmem_cols);
 }
 
-// Joins the parts of the groups that more than one CTA worked on.  Block
-// (i, c) joins row c of the group that the border after CTA i's share cuts,
-// if CTA i is the first to work on that group; four values a thread.
+// Joins the parts of the groups that more than one CTA worked on, one row a
+// block, four values a thread; the first CTA of every such group has left in
+// `cuts` which CTAs those are.
 __global__ void __launch_bounds__(128) latent_join_kernel(const __grid_constant__ LatentMmaArgs a) {
   pdl_begin();
-  const int64_t i0 = blockIdx.x;
+  const int4 cut = a.cuts[blockIdx.x];            // first row, rows, first CTA, last CTA
   const int c = blockIdx.y, lane = threadIdx.x & 31;
-  const int64_t total = total_tiles(a, lane);
-  const int64_t n = shares(a, total);
-  if (i0 >= n) return;
-  const int64_t border = total * (i0 + 1) / n;
-  const Place p = locate(a, border - 1, lane);
-  if (p.tile + 1 == p.tiles || p.g * a.N + c >= a.rows) return;
-  // the share that holds tile x is the largest i with total * i / n <= x
-  const int64_t first = border - 1 - p.tile, last = first + p.tiles - 1;
-  if (((first + 1) * n - 1) / total != i0) return;
-  const int64_t i1 = ((last + 1) * n - 1) / total;
+  if (c >= cut.y) return;
+  const int64_t i0 = cut.z, i1 = cut.w;
   auto slot = [&](int64_t i) { return 2 * i + (i == i0 ? 1 : 0); };
   const int d = threadIdx.x * 4;
   float M = kNoMax, L = 0.f;
@@ -707,7 +794,7 @@ __global__ void __launch_bounds__(128) latent_join_kernel(const __grid_constant_
       }
     }
   }
-  const int64_t row = static_cast<int64_t>(p.b) * a.rows + p.g * a.N + c;
+  const int64_t row = static_cast<int64_t>(cut.x) + c;
   const float inv = L > 0.f ? 1.f / L : 0.f;
   const float v[4] = {s.x * inv, s.y * inv, s.z * inv, s.w * inv};
   __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out) + row * a.d_v + d;
@@ -743,7 +830,7 @@ bool latent_mma_layout(LatentMmaArgs* a, int num_sms, int max_smem) {
   const int64_t q = static_cast<int64_t>(a->nb) * a->N * 128;
   const int64_t room = static_cast<int64_t>(max_smem) - 1024 - q - static_cast<int64_t>(sizeof(Smem));
   a->bufs = static_cast<int>(std::min<int64_t>(kMaxBufs, room / (static_cast<int64_t>(a->slots) * kBlockBytes)));
-  if (a->bufs < 1 || a->slots > kMaxBlocks) return false;
+  if (a->bufs < 1 || a->slots > kMaxSlots) return false;
   a->s_bufs = a->bufs >= 2 ? 2 : 1;
   // one CTA an SM: tensor memory is taken in full
   a->smem_bytes = static_cast<uint32_t>(std::max<int64_t>(
@@ -753,6 +840,10 @@ bool latent_mma_layout(LatentMmaArgs* a, int num_sms, int max_smem) {
   const int64_t cap = a->sel ? a->k : static_cast<int64_t>(a->max_pages) * a->page_size;
   const int64_t most = static_cast<int64_t>(a->seqs) * a->groups * ((cap + kTile - 1) / kTile);
   a->grid = static_cast<int>(std::min<int64_t>(num_sms, most));
+  // a cut for every border between shares, or for every group where those are fewer
+  const int64_t n_groups = static_cast<int64_t>(a->seqs) * a->groups;
+  a->cuts_by_group = n_groups < a->grid - 1;
+  a->n_cuts = static_cast<int>(std::min<int64_t>(n_groups, a->grid - 1));
   return true;
 }
 
@@ -761,7 +852,7 @@ cudaError_t launch_latent_mma(const LatentMmaArgs& a, cudaStream_t st) {
 }
 
 cudaError_t launch_latent_join(const LatentMmaArgs& a, cudaStream_t st) {
-  return launch_pdl(latent_join_kernel, dim3(a.grid - 1, std::min(a.N, a.rows)), dim3(128), 0, st, 1, a);
+  return launch_pdl(latent_join_kernel, dim3(a.n_cuts, std::min(a.N, a.rows)), dim3(128), 0, st, 1, a);
 }
 
 }  // namespace li

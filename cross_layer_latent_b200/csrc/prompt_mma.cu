@@ -14,7 +14,9 @@
 // Tensor memory is full: S0, S1 (P takes the place of S), O0, O1.  Shared
 // memory holds both query tiles (96 KB) and a ring of 16 KB blocks, 128
 // tokens x 64 columns of K (k_nope of the head, then the k_rope that all heads
-// share) or of V; blocks are freed one by one.
+// share) or of V.  A key tile has two parts in the ring, its K blocks and its
+// V blocks, each with one barrier: eight blocks hold 1.6 tiles, and a part is
+// loaded at least 1280 cycles of MMA before it is needed.
 //
 // The running maximum moves only when a row exceeds it by more than 8 (in
 // powers of two): weights stay below 256, which costs their bf16 rounding
@@ -40,6 +42,7 @@ constexpr int kSoftWarps = 8;                    // a warpgroup for each query t
 constexpr int kMmaWarp = 8, kLoadWarp = 9;   // and one that zeroes
 constexpr int kThreads = 32 * 11;
 constexpr int kMaxRing = 13;
+constexpr int kParts = 8;                        // parts in flight at most (a power of two)
 constexpr float kGrow = 8.f;
 constexpr float kNoMax = -1e30f;
 constexpr uint64_t kDrainNs = 1000ull * 1000ull;
@@ -51,7 +54,7 @@ struct Unit {
 };
 
 struct Smem {
-  uint64_t full[kMaxRing], empty[kMaxRing], raw[kMaxRing];
+  uint64_t full[kParts], empty[kParts], raw[kParts];
   uint64_t unit_full[2], unit_empty[2];
   uint64_t q_full, q_empty, s_full[2], p_full[2], o_full[2], o_empty[2], drain;
   Unit unit[2];
@@ -136,7 +139,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_mma_kernel(const __grid_co
   const WaitCtl wc{&sm.abort_flag, a.status, a.wait_ns};
 
   if (threadIdx.x == 0) {
-    for (int i = 0; i < a.ring; ++i) {
+    for (int i = 0; i < kParts; ++i) {
       mbar_init(&sm.full[i], 1);
       mbar_init(&sm.empty[i], 1);
       mbar_init(&sm.raw[i], 1);
@@ -176,10 +179,10 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_mma_kernel(const __grid_co
     const uint32_t lanes = static_cast<uint32_t>(quad * 32) << 16;
     const uint32_t s_tm = tmem + q * 128 + lanes, o_tm = tmem + 256 + q * 128 + lanes;
     const int r = quad * 32 + lane;
-    int64_t tile = 0, outs = 0;
+    uint32_t tile = 0, outs = 0;
     bool ok = true;
-    for (int64_t un = 0; ok; ++un) {
-      ok = __all_sync(0xffffffffu, bounded_wait_sleep(&sm.unit_full[un & 1], static_cast<uint32_t>(un >> 1) & 1u, wc));
+    for (uint32_t un = 0; ok; ++un) {
+      ok = __all_sync(0xffffffffu, bounded_wait_sleep(&sm.unit_full[un & 1], (un >> 1) & 1u, wc));
       if (!ok) break;
       const Unit u = sm.unit[un & 1];
       __syncwarp();
@@ -191,7 +194,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_mma_kernel(const __grid_co
       const int lim = i < u.nq ? key_limit(a, u, i) : u.nk;
       float m = kNoMax, l = 0.f;
       for (int t = 0; t < n; ++t, ++tile) {
-        ok = __all_sync(0xffffffffu, bounded_wait(&sm.s_full[q], static_cast<uint32_t>(tile) & 1u, wc));
+        ok = __all_sync(0xffffffffu, bounded_wait(&sm.s_full[q], tile & 1u, wc));
         if (!ok) break;
         tc_fence_after();
         float x[128];
@@ -213,10 +216,12 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_mma_kernel(const __grid_co
           for (int c = 0; c < 128; ++c)
             if (c >= left) x[c] = -INFINITY;
         }
-        float top = x[0];
+        float top4[4] = {x[0], x[1], x[2], x[3]};
 #pragma unroll
-        for (int c = 1; c < 127; c += 2) top = fmaxf(fmaxf(top, x[c]), x[c + 1]);
-        top = fmaxf(top, x[127]);
+        for (int c = 4; c < 124; c += 8)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) top4[e] = fmaxf(fmaxf(top4[e], x[c + e]), x[c + 4 + e]);
+        const float top = fmaxf(fmaxf(fmaxf(top4[0], x[124]), fmaxf(top4[1], x[125])), fmaxf(fmaxf(top4[2], x[126]), fmaxf(top4[3], x[127])));
         const bool grow = (top - m) * a.scale_log2 > kGrow;
         if (__any_sync(0xffffffffu, grow)) {
           const float now = grow ? top : m;
@@ -260,7 +265,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_mma_kernel(const __grid_co
       if (!ok) break;
       if (first >= u.nq) continue;
       if (n > 0) {
-        ok = __all_sync(0xffffffffu, bounded_wait(&sm.o_full[q], static_cast<uint32_t>(outs) & 1u, wc));
+        ok = __all_sync(0xffffffffu, bounded_wait(&sm.o_full[q], outs & 1u, wc));
         if (!ok) break;
         ++outs;
         tc_fence_after();
@@ -303,77 +308,91 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_mma_kernel(const __grid_co
     if (elect_one()) {
       const uint32_t id_s = make_instr_desc(1, 128, 128);
       const uint32_t id_o = make_instr_desc(1, 128, 64) | kMajorMnB;
-      const uint32_t q_smem = smem_addr(base), ring_smem = smem_addr(ring);
-      int64_t blocks = 0;                        // ring position of the unit's first block
-      int64_t ptile[2] = {0, 0}, outs[2] = {0, 0};
-      bool ok = true;
-      auto slot_of = [&](int64_t i, uint32_t* ph) {
-        *ph = static_cast<uint32_t>(i / a.ring) & 1u;
-        return static_cast<int>(i % a.ring);
-      };
+      const uint32_t q0 = desc_lo(smem_addr(base), 0), r0 = desc_lo(smem_addr(ring), 0);
+      constexpr uint32_t kBlockStep = kBlockBytes >> 4;
       const int per = nkb + a.v_blocks;
-      for (int64_t un = 0, busy = 0; ok; ++un) {
-        if (!(ok = bounded_wait(&sm.unit_full[un & 1], static_cast<uint32_t>(un >> 1) & 1u, wc))) break;
+      int kc = 0, vc = nkb;                      // ring positions of the next K part and V part
+      uint32_t kp = 0, vp = 1;                   // and their numbers
+      auto advance = [&](int& c, uint32_t& p) {
+        c += per;
+        if (c >= a.ring) c -= a.ring;
+        p += 2;
+      };
+      uint32_t ptile[2] = {0, 0}, outs[2] = {0, 0};
+      bool ok = true;
+      if (vc >= a.ring) vc -= a.ring;
+      uint32_t busy = 0;
+      for (uint32_t un = 0; ok; ++un) {
+        if (!(ok = bounded_wait(&sm.unit_full[un & 1], (un >> 1) & 1u, wc))) break;
         const Unit u = sm.unit[un & 1];
         mbar_arrive(&sm.unit_empty[un & 1]);
         if (u.h < 0) break;
-        const int n[2] = {key_tiles(a, u, 0), key_tiles(a, u, 1)};
-        const int nt = max(n[0], n[1]);
+        const int n0 = key_tiles(a, u, 0), n1 = key_tiles(a, u, 1), nt = max(n0, n1);
         if (nt == 0) continue;
-        if (!(ok = bounded_wait(&sm.q_full, static_cast<uint32_t>(busy) & 1u, wc))) break;
+        if (!(ok = bounded_wait(&sm.q_full, busy & 1u, wc))) break;
         ++busy;
-        auto scores = [&](int q, int t, bool last) {
-          for (int j = 0; j < nkb; ++j) {
-            uint32_t ph;
-            const int s = slot_of(blocks + static_cast<int64_t>(t) * per + j, &ph);
-            if (!bounded_wait(&sm.full[s], ph, wc)) return false;
-            tc_fence_after();
-            const uint64_t da = desc_sw128(q_smem + (q * nkb + j) * kBlockBytes, 16, 1024);
-            const uint64_t db = desc_sw128(ring_smem + s * kBlockBytes, 16, 1024);
+        bool k_here = false, v_here = false;
+        // S_q of the next K part; `last`: no other tile needs the part
+        auto scores = [&](int q, bool last) {
+          if (!k_here && !bounded_wait(&sm.full[kp % kParts], (kp / kParts) & 1u, wc)) return false;
+          k_here = true;
+          tc_fence_after();
+          uint32_t da = q0 + q * nkb * kBlockStep;
+          int s = kc;
+          for (int j = 0; j < nkb; ++j, da += kBlockStep) {
+            const uint32_t db = r0 + s * kBlockStep;
+            if (++s == a.ring) s = 0;
             const int ks = j == a.nope_blocks - 1 ? a.nope_ksteps : (j == nkb - 1 ? a.rope_ksteps : 4);
-#pragma unroll
-            for (int kk = 0; kk < 4; ++kk)
-              if (kk < ks) umma<kKindBF16>(tmem + q * 128, da + 2 * kk, db + 2 * kk, id_s, (j > 0 || kk > 0) ? 1u : 0u);
-            if (last) umma_commit(&sm.empty[s]);
+            if (ks == 4) {
+              umma_ss_steps<4, 2, 2>(tmem + q * 128, da, db, id_s, j > 0 ? 1u : 0u);
+            } else {
+              for (int k = 0; k < ks; ++k) umma_ss_steps<1, 2, 2>(tmem + q * 128, da + 2 * k, db + 2 * k, id_s, j + k > 0 ? 1u : 0u);
+            }
+          }
+          if (last) {
+            umma_commit(&sm.empty[kp % kParts]);
+            advance(kc, kp);
+            k_here = false;
           }
           umma_commit(&sm.s_full[q]);
           return true;
         };
-        auto values = [&](int q, int t, bool last) {
-          if (t == 0 && outs[q] > 0 && !bounded_wait(&sm.o_empty[q], static_cast<uint32_t>(outs[q] - 1) & 1u, wc)) return false;
-          if (!bounded_wait(&sm.p_full[q], static_cast<uint32_t>(ptile[q]) & 1u, wc)) return false;
+        // O_q of the next V part
+        auto values = [&](int q, bool first, bool final, bool last) {
+          if (first && outs[q] > 0 && !bounded_wait(&sm.o_empty[q], (outs[q] - 1) & 1u, wc)) return false;
+          if (!v_here && !bounded_wait(&sm.full[vp % kParts], (vp / kParts) & 1u, wc)) return false;
+          v_here = true;
+          if (!bounded_wait(&sm.p_full[q], ptile[q] & 1u, wc)) return false;
           ++ptile[q];
           tc_fence_after();
+          int s = vc;
           for (int j = 0; j < a.v_blocks; ++j) {
-            uint32_t ph;
-            const int s = slot_of(blocks + static_cast<int64_t>(t) * per + nkb + j, &ph);
-            if (!bounded_wait(&sm.full[s], ph, wc)) return false;
-            tc_fence_after();
-            const uint64_t dv = desc_sw128(ring_smem + s * kBlockBytes, 16, 1024);
-#pragma unroll
-            for (int kk = 0; kk < 8; ++kk)
-              umma_ts_bf16(tmem + 256 + q * 128 + j * 64, tmem + q * 128 + kk * 8, dv + kk * 128, id_o, (t > 0 || kk > 0) ? 1u : 0u);
-            if (last) umma_commit(&sm.empty[s]);
+            umma_ts_steps<8, 128>(tmem + 256 + q * 128 + j * 64, tmem + q * 128, r0 + s * kBlockStep, id_o, first ? 0u : 1u);
+            if (++s == a.ring) s = 0;
           }
-          if (t == n[q] - 1) {
+          if (last) {
+            umma_commit(&sm.empty[vp % kParts]);
+            advance(vc, vp);
+            v_here = false;
+          }
+          if (final) {
             umma_commit(&sm.o_full[q]);
             ++outs[q];
           }
           return true;
         };
-        // a block is free after the last of the two tiles that use it
-        for (int q = 0; q < 2 && ok; ++q)
-          if (n[q] > 0) ok = scores(q, 0, q == 1 || n[1] == 0);
+        if (n0 > 0) ok = scores(0, n1 == 0);
+        if (ok && n1 > 0) ok = scores(1, true);
         if (ok && nt == 1) umma_commit(&sm.q_empty);
         for (int t = 0; t < nt && ok; ++t) {
-          for (int q = 0; q < 2 && ok; ++q) {
-            if (t < n[q]) ok = values(q, t, q == 1 || t >= n[1]);
-            if (ok && t + 1 < n[q]) ok = scores(q, t + 1, q == 1 || t + 1 >= n[1]);
-          }
+          if (t < n0) ok = values(0, t == 0, t == n0 - 1, t >= n1);
+          if (ok && t + 1 < n0) ok = scores(0, t + 1 >= n1);
+          if (ok && t < n1) ok = values(1, t == 0, t == n1 - 1, true);
+          if (ok && t + 1 < n1) ok = scores(1, true);
           if (ok && t + 2 == nt) umma_commit(&sm.q_empty);
         }
-        blocks += static_cast<int64_t>(nt) * per;
       }
+      // nothing is in flight when the CTA ends, whichever role gave up
       umma_commit(&sm.drain);
       drain_wait(&sm.drain, 0, kDrainNs);
     }
@@ -385,13 +404,15 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_mma_kernel(const __grid_co
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) units += __shfl_xor_sync(0xffffffffu, units, o);
     const int64_t total = units * a.H;
-    int64_t next = blockIdx.x, blk = 0, queries = 0;
+    int64_t next = blockIdx.x;
+    uint32_t part = 0, tail = 0, busy = 0;       // parts loaded, parts known to be free again, units with keys
+    int free_blocks = a.ring, slot = 0;
     bool ok = true;
-    for (int64_t un = 0, busy = 0; ok; ++un) {
+    for (uint32_t un = 0; ok; ++un) {
       const Unit u = find_unit(a, next, total, lane);
       if (u.h >= 0 && lane == 0) next = static_cast<int64_t>(gridDim.x) + atomicAdd(a.next_unit, 1u);
       next = __shfl_sync(0xffffffffu, next, 0);
-      if (un >= 2) ok = __all_sync(0xffffffffu, bounded_wait(&sm.unit_empty[un & 1], static_cast<uint32_t>((un >> 1) - 1) & 1u, wc));
+      if (un >= 2) ok = __all_sync(0xffffffffu, bounded_wait(&sm.unit_empty[un & 1], ((un >> 1) - 1) & 1u, wc));
       if (!ok) break;
       if (lane == 0) {
         sm.unit[un & 1] = u;
@@ -402,72 +423,90 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_mma_kernel(const __grid_co
       if (nt == 0) continue;
       int good = 1;
       if (lane == 0) {
-        if (busy > 0) good = bounded_wait(&sm.q_empty, static_cast<uint32_t>(busy - 1) & 1u, wc);
+        // a part of `blocks` blocks of the ring, once they are free
+        auto room = [&](int blocks) {
+          while (free_blocks < blocks || part - tail >= kParts) {
+            if (!bounded_wait(&sm.empty[tail % kParts], (tail / kParts) & 1u, wc)) return false;
+            free_blocks += tail & 1 ? a.v_blocks : nkb;
+            ++tail;
+          }
+          free_blocks -= blocks;
+          return true;
+        };
+        auto next_slot = [&]() {
+          uint8_t* p = ring + slot * kBlockBytes;
+          if (++slot == a.ring) slot = 0;
+          return p;
+        };
+        if (busy > 0) good = bounded_wait(&sm.q_empty, (busy - 1) & 1u, wc);
         if (good) {
           const int tiles = n1 > 0 ? 2 : 1;
           mbar_arrive_expect_tx(&sm.q_full, tiles * nkb * kBlockBytes);
-          ++queries;
+          ++busy;
           for (int q = 0; q < tiles; ++q)
             for (int j = 0; j < nkb; ++j)
               tma_load_3d(base + (q * nkb + j) * kBlockBytes, &a.map_q, &sm.q_full,
                           j < a.nope_blocks ? 64 * j : a.d_nope + 64 * (j - a.nope_blocks), u.h, u.q0 + u.row0 + q * kTile);
-          for (int t = 0; t < nt && good; ++t) {
+          for (int t = 0; t < nt; ++t) {
             const int row = u.k0 + t * kTile;
-            for (int j = 0; j < nkb + a.v_blocks && good; ++j, ++blk) {
-              const int s = static_cast<int>(blk % a.ring);
-              const int64_t use = blk / a.ring;
-              if (use > 0) good = bounded_wait(&sm.empty[s], static_cast<uint32_t>(use - 1) & 1u, wc);
-              if (!good) break;
-              uint8_t* dst = ring + s * kBlockBytes;
-              // values past the sequence's end are zeroed before anyone reads them
-              uint64_t* bar = j >= nkb && (t + 1) * kTile > u.nk ? &sm.raw[s] : &sm.full[s];
-              mbar_arrive_expect_tx(bar, kBlockBytes);
-              if (j < a.nope_blocks) tma_load_3d(dst, &a.map_k, bar, 64 * j, u.h, row);
-              else if (j < nkb) tma_load_2d(dst, &a.map_kr, bar, 64 * (j - a.nope_blocks), row);
-              else tma_load_3d(dst, &a.map_v, bar, 64 * (j - nkb), u.h, row);
+            if (!(good = room(nkb))) break;
+            uint64_t* bar = &sm.full[part % kParts];
+            mbar_arrive_expect_tx(bar, nkb * kBlockBytes);
+            for (int j = 0; j < nkb; ++j) {
+              if (j < a.nope_blocks) tma_load_3d(next_slot(), &a.map_k, bar, 64 * j, u.h, row);
+              else tma_load_2d(next_slot(), &a.map_kr, bar, 64 * (j - a.nope_blocks), row);
             }
+            ++part;
+            if (!(good = room(a.v_blocks))) break;
+            // values past the sequence's end are zeroed before anyone reads them
+            bar = (t + 1) * kTile > u.nk ? &sm.raw[part % kParts] : &sm.full[part % kParts];
+            mbar_arrive_expect_tx(bar, a.v_blocks * kBlockBytes);
+            for (int j = 0; j < a.v_blocks; ++j) tma_load_3d(next_slot(), &a.map_v, bar, 64 * j, u.h, row);
+            ++part;
           }
         }
       }
       ok = __shfl_sync(0xffffffffu, good, 0) != 0;
-      ++busy;
     }
     if (lane == 0) {
-      // the copies in flight land before the CTA ends, whichever role gave up
-      for (int64_t f = max(blk - a.ring, int64_t(0)); f < blk; ++f)
-        drain_wait(&sm.full[f % a.ring], static_cast<uint32_t>(f / a.ring) & 1u, kDrainNs);
-      if (queries > 0) drain_wait(&sm.q_full, static_cast<uint32_t>(queries - 1) & 1u, kDrainNs);
+      // the copies that were issued land before the CTA ends, whichever role gave up
+      for (uint32_t f = part > kParts ? part - kParts : 0; f < part; ++f)
+        drain_wait(&sm.full[f % kParts], (f / kParts) & 1u, kDrainNs);
+      if (busy > 0) drain_wait(&sm.q_full, (busy - 1) & 1u, kDrainNs);
     }
     __syncwarp();
   } else {
     // ------------------------------------------------ zeroes behind a sequence's last values
-    int64_t blocks = 0;
-    uint32_t raw_phase = 0;
+    int vc = nkb % a.ring;                       // ring position of the unit's first V part
+    uint32_t vp = 1, raw_phase = 0;
+    const int per = nkb + a.v_blocks;
     bool ok = true;
-    for (int64_t un = 0; ok; ++un) {
-      ok = __all_sync(0xffffffffu, bounded_wait_sleep(&sm.unit_full[un & 1], static_cast<uint32_t>(un >> 1) & 1u, wc));
+    for (uint32_t un = 0; ok; ++un) {
+      ok = __all_sync(0xffffffffu, bounded_wait_sleep(&sm.unit_full[un & 1], (un >> 1) & 1u, wc));
       if (!ok) break;
       const Unit u = sm.unit[un & 1];
       __syncwarp();
       if (lane == 0) mbar_arrive(&sm.unit_empty[un & 1]);
       if (u.h < 0) break;
       const int nt = max(key_tiles(a, u, 0), key_tiles(a, u, 1));
-      const int per = nkb + a.v_blocks;
       if (nt > 0 && nt * kTile > u.nk) {
+        const uint32_t p = vp + 2 * (nt - 1);
         const int keep = u.nk - (nt - 1) * kTile;
-        for (int j = 0; j < a.v_blocks && ok; ++j) {
-          const int s = static_cast<int>((blocks + static_cast<int64_t>(nt - 1) * per + nkb + j) % a.ring);
-          ok = __all_sync(0xffffffffu, bounded_wait_sleep(&sm.raw[s], (raw_phase >> s) & 1u, wc));
-          if (!ok) break;
-          raw_phase ^= 1u << s;
+        int s = (vc + (nt - 1) * per) % a.ring;
+        ok = __all_sync(0xffffffffu, bounded_wait_sleep(&sm.raw[p % kParts], (raw_phase >> (p % kParts)) & 1u, wc));
+        if (!ok) break;
+        raw_phase ^= 1u << (p % kParts);
+        for (int j = 0; j < a.v_blocks; ++j) {
           uint4* rows = reinterpret_cast<uint4*>(ring + s * kBlockBytes);
           for (int x = keep * 8 + lane; x < kTile * 8; x += 32) rows[x] = make_uint4(0u, 0u, 0u, 0u);
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&sm.full[s]);
+          if (++s == a.ring) s = 0;
         }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.full[p % kParts]);
       }
-      blocks += static_cast<int64_t>(nt) * per;
+      vc = (vc + nt * per) % a.ring;
+      vp += 2 * nt;
     }
   }
   tc_fence_before();
