@@ -137,6 +137,49 @@ __device__ __forceinline__ float exp2_fast(float x) {
   return r;
 }
 
+// Paired fp32 arithmetic (one instruction for two IEEE operations).
+__device__ __forceinline__ uint64_t pair(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ float2 unpair(uint64_t p) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(p));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
+// 2^x of a pair on the FMA pipes, for x <= 100: x = n + r with |r| <= 1/2, a
+// polynomial for 2^r and n added to its exponent.  The coefficients are the
+// best of degree 4 for the relative error on [-1/2, 1/2] (a Remez exchange):
+// 2.7e-6, 4e-8 on average, a two-hundredth of the rounding to bf16 that
+// follows.  x below -126 counts as -126.
+__device__ __forceinline__ float2 exp2_poly(uint64_t x) {
+  float2 v = unpair(x);
+  const uint64_t y = pair(fmaxf(v.x, -126.f), fmaxf(v.y, -126.f));
+  const uint64_t big = pair(12582912.f, 12582912.f), less = pair(-12582912.f, -12582912.f);   // 1.5 * 2^23: rounds to whole
+  const uint64_t n = add2(y, big);
+  const uint64_t whole = add2(n, less);
+  const uint64_t r = fma2(whole, pair(-1.f, -1.f), y);
+  uint64_t p = fma2(pair(0.009570102207362652f, 0.009570102207362652f), r, pair(0.05591785907745361f, 0.05591785907745361f));
+  p = fma2(p, r, pair(0.240247443318367f, 0.240247443318367f));
+  p = fma2(p, r, pair(0.6931217908859253f, 0.6931217908859253f));
+  p = fma2(p, r, pair(0.9999992847442627f, 0.9999992847442627f));
+  const float2 m = unpair(p), e = unpair(n);
+  return make_float2(__int_as_float(__float_as_int(m.x) + (__float_as_int(e.x) << 23)),
+                     __int_as_float(__float_as_int(m.y) + (__float_as_int(e.y) << 23)));
+}
+
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   uint32_t r;
   asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));

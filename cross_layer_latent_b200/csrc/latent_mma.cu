@@ -500,66 +500,55 @@ __global__ void __launch_bounds__(kThreads, 1) latent_mma_kernel(const __grid_co
       const uint32_t c0 = desc_lo(tiles_smem, 0), q0 = desc_lo(q_smem, 0), v0 = desc_lo(tiles_smem, kBlockBytes);
       constexpr uint32_t kBlockStep = kBlockBytes >> 4, kQStep = (N * 128) >> 4;
       const uint32_t tile_step = a.slots * kBlockStep;
-      // S^T of the next tile, part p
-      auto scores = [&](int p) {
-        if (!bounded_wait(&sm.full[sr.buf][p], sr.ph, wc)) return false;
-        fence_proxy_async_smem();                // rows gathered by cp.async are read by the tensor cores
-        tc_fence_after();
-        const uint32_t d = s_tmem + ssr.buf * N;
-        const int end = p == 0 ? min(kHalf, a.nb) : a.nb;
-        uint32_t c = c0 + sr.buf * tile_step + p * kHalf * kBlockStep, q = q0 + p * kHalf * kQStep;
-        for (int j = p * kHalf; j < end; ++j, c += kBlockStep, q += kQStep) {
-          if (j < a.nb - 1 || a.last_ksteps == 4) {
-            umma_ss_steps<4, 2, 2>(d, c, q, id_s, j > 0 ? 1u : 0u);
-          } else {
-            for (int k = 0; k < a.last_ksteps; ++k) umma_ss_steps<1, 2, 2>(d, c + 2 * k, q + 2 * k, id_s, j + k > 0 ? 1u : 0u);
-          }
-        }
-        if (p == parts - 1) {
-          umma_commit(&sm.s_full[ssr.buf]);
-          sr.step(a.bufs);
-          ssr.step(a.s_bufs);
-        }
-        return true;
-      };
       for (bool more = w.start(a, sm); more && ok; more = w.next(a), ++seg) {
         if (!(ok = bounded_wait(&sm.q_full, seg & 1u, wc))) break;
+        if (seg > 0 && !(ok = bounded_wait(&sm.o_empty, (seg - 1) & 1u, wc))) break;
         const int nt = w.s.t1 - w.s.t0;
-        int issued = 0, part = 0;                // tiles whose scores are issued, parts of the next one
-        auto next_scores = [&]() {
-          ok = scores(part);
-          if (++part == parts) {
-            part = 0;
-            if (++issued == nt) umma_commit(&sm.q_empty);
-          }
-        };
-        for (int t = 0; t < nt && ok; ++t) {
-          while (ok && issued == t) next_scores();
-          if (!ok) break;
-          // the next tile's scores go first, part by part, as far as that tile is here before this one's weights are
-          if (a.s_bufs == 2 && issued < nt) {
-            const uint64_t began = cycles();
-            while (ok && issued == t + 1 && issued < nt && !mbar_test_wait(&sm.p_full[vsr.buf], vsr.ph)) {
-              if (mbar_test_wait(&sm.full[sr.buf][part], sr.ph)) next_scores();
-              else if (*wc.abort_flag || cycles() - began > a.wait_ns * kCyclesPerNs) ok = give_up(wc);
+        // One step at a time, so that each kind's code stays small and warm: the products with the values as
+        // soon as the weights are there, else the next tile's scores, part by part, as far as the tile is here.
+        int st = 0, part = 0, vt = 0;            // tiles whose scores are issued, parts of the next, tiles done
+        uint64_t idle = cycles();
+        while (vt < nt) {
+          if (vt < st && mbar_test_wait(&sm.p_full[vsr.buf], vsr.ph)) {
+            tc_fence_after();
+            const uint32_t v = v0 + vr.buf * tile_step, pt = v + (a.slots - 1) * kBlockStep;
+            uint64_t* const empty = sm.empty[vr.buf];
+            for (int mb = 0; mb < a.m_blocks; ++mb) {
+              umma_ss_steps<kTile / 16, 128, 128>(o_tmem + mb * N, v + 2 * mb * kBlockStep, pt, id_o, vt > 0 ? 1u : 0u);
+              if (2 * (mb + 1) == kHalf && parts == 2 && mb < a.m_blocks - 1) umma_commit(&empty[0]);
             }
+            if (parts == 1 || 2 * a.m_blocks <= kHalf) umma_commit(&empty[0]);
+            if (parts == 2) umma_commit(&empty[1]);
+            umma_commit(&sm.pv_done);
+            vr.step(a.bufs);
+            vsr.step(a.s_bufs);
+            if (++vt == nt) umma_commit(&sm.o_full);
+          } else if (st < nt && st < vt + a.s_bufs && mbar_test_wait(&sm.full[sr.buf][part], sr.ph)) {
+            fence_proxy_async_smem();            // rows gathered by cp.async are read by the tensor cores
+            tc_fence_after();
+            const uint32_t d = s_tmem + ssr.buf * N;
+            const int end = part == 0 ? min(kHalf, a.nb) : a.nb;
+            uint32_t c = c0 + sr.buf * tile_step + part * kHalf * kBlockStep, q = q0 + part * kHalf * kQStep;
+            for (int j = part * kHalf; j < end; ++j, c += kBlockStep, q += kQStep) {
+              if (j < a.nb - 1 || a.last_ksteps == 4) {
+                umma_ss_steps<4, 2, 2>(d, c, q, id_s, j > 0 ? 1u : 0u);
+              } else {
+                for (int k = 0; k < a.last_ksteps; ++k) umma_ss_steps<1, 2, 2>(d, c + 2 * k, q + 2 * k, id_s, j + k > 0 ? 1u : 0u);
+              }
+            }
+            if (++part == parts) {
+              umma_commit(&sm.s_full[ssr.buf]);
+              sr.step(a.bufs);
+              ssr.step(a.s_bufs);
+              part = 0;
+              if (++st == nt) umma_commit(&sm.q_empty);
+            }
+          } else {
+            if (!*wc.abort_flag && cycles() - idle <= a.wait_ns * kCyclesPerNs) continue;
+            ok = give_up(wc);
+            break;
           }
-          if (!ok) break;
-          if (t == 0 && seg > 0 && !(ok = bounded_wait(&sm.o_empty, (seg - 1) & 1u, wc))) break;
-          if (!(ok = bounded_wait(&sm.p_full[vsr.buf], vsr.ph, wc))) break;
-          tc_fence_after();
-          const uint32_t v = v0 + vr.buf * tile_step, pt = v + (a.slots - 1) * kBlockStep;
-          uint64_t* const empty = sm.empty[vr.buf];
-          for (int mb = 0; mb < a.m_blocks; ++mb) {
-            umma_ss_steps<kTile / 16, 128, 128>(o_tmem + mb * N, v + 2 * mb * kBlockStep, pt, id_o, t > 0 ? 1u : 0u);
-            if (2 * (mb + 1) == kHalf && parts == 2 && mb < a.m_blocks - 1) umma_commit(&empty[0]);
-          }
-          if (parts == 1 || 2 * a.m_blocks <= kHalf) umma_commit(&empty[0]);
-          if (parts == 2) umma_commit(&empty[1]);
-          umma_commit(&sm.pv_done);
-          if (t == nt - 1) umma_commit(&sm.o_full);
-          vr.step(a.bufs);
-          vsr.step(a.s_bufs);
+          idle = cycles();
         }
       }
       // nothing is in flight when the CTA ends, whichever role gave up

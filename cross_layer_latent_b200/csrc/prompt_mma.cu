@@ -43,6 +43,7 @@ constexpr int kMmaWarp = 8, kLoadWarp = 9;   // and one that zeroes
 constexpr int kThreads = 32 * 11;
 constexpr int kMaxRing = 13;
 constexpr int kParts = 8;                        // parts in flight at most (a power of two)
+constexpr int kPolyAt = 2;                       // of every three pairs of exponentials one is computed on the FMA pipes
 constexpr float kGrow = 8.f;
 constexpr float kNoMax = -1e30f;
 constexpr uint64_t kDrainNs = 1000ull * 1000ull;
@@ -56,7 +57,7 @@ struct Unit {
 struct Smem {
   uint64_t full[kParts], empty[kParts], raw[kParts];
   uint64_t unit_full[2], unit_empty[2];
-  uint64_t q_full, q_empty, s_full[2], p_full[2], o_full[2], o_empty[2], drain;
+  uint64_t q_full, q_empty, s_full[2], p_full[2][2], o_full[2], o_empty[2], drain;
   Unit unit[2];
   uint32_t tmem;
   int abort_flag;
@@ -148,7 +149,8 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_mma_kernel(const __grid_co
       mbar_init(&sm.unit_full[i], 1);
       mbar_init(&sm.unit_empty[i], kSoftWarps + 2);
       mbar_init(&sm.s_full[i], 1);
-      mbar_init(&sm.p_full[i], 4);
+      mbar_init(&sm.p_full[i][0], 4);
+      mbar_init(&sm.p_full[i][1], 4);
       mbar_init(&sm.o_full[i], 1);
       mbar_init(&sm.o_empty[i], 4);
     }
@@ -198,30 +200,40 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_mma_kernel(const __grid_co
         if (!ok) break;
         tc_fence_after();
         float x[128];
-        {
-          uint32_t xr[4][32];
+        const int left = lim - t * kTile;
+        const bool mask = __any_sync(0xffffffffu, left < kTile);
+        float top4[4];
+        uint32_t xr[2][32];
+        tmem_ld<32>(s_tm, xr[0]);
+        tmem_wait_ld();
 #pragma unroll
-          for (int c = 0; c < 4; ++c) tmem_ld<32>(s_tm + 32 * c, xr[c]);
-          tmem_wait_ld();
+        for (int c = 0; c < 4; ++c) {
+          // a quarter's maximum while the next quarter is on its way
+          if (c < 3) tmem_ld<32>(s_tm + 32 * (c + 1), xr[(c + 1) & 1]);
 #pragma unroll
-          for (int c = 0; c < 128; ++c) x[c] = __uint_as_float(xr[c / 32][c % 32]);
+          for (int e = 0; e < 32; ++e) {
+            x[32 * c + e] = __uint_as_float(xr[c & 1][e]);
+            if (a.negate) x[32 * c + e] = -x[32 * c + e];
+          }
+          if (mask) {
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              if (32 * c + e >= left) x[32 * c + e] = -INFINITY;
+          }
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            if (c == 0) top4[e] = x[e];
+            else top4[e] = fmaxf(top4[e], x[32 * c + e]);
+          }
+#pragma unroll
+          for (int i = 4; i < 28; i += 8)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) top4[e] = fmaxf(fmaxf(top4[e], x[32 * c + i + e]), x[32 * c + i + 4 + e]);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) top4[e] = fmaxf(top4[e], x[32 * c + 28 + e]);
+          if (c < 3) tmem_wait_ld();
         }
-        if (a.negate) {
-#pragma unroll
-          for (int c = 0; c < 128; ++c) x[c] = -x[c];
-        }
-        if (__any_sync(0xffffffffu, (t + 1) * kTile > lim)) {
-          const int left = lim - t * kTile;
-#pragma unroll
-          for (int c = 0; c < 128; ++c)
-            if (c >= left) x[c] = -INFINITY;
-        }
-        float top4[4] = {x[0], x[1], x[2], x[3]};
-#pragma unroll
-        for (int c = 4; c < 124; c += 8)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) top4[e] = fmaxf(fmaxf(top4[e], x[c + e]), x[c + 4 + e]);
-        const float top = fmaxf(fmaxf(fmaxf(top4[0], x[124]), fmaxf(top4[1], x[125])), fmaxf(fmaxf(top4[2], x[126]), fmaxf(top4[3], x[127])));
+        const float top = fmaxf(fmaxf(top4[0], top4[1]), fmaxf(top4[2], top4[3]));
         const bool grow = (top - m) * a.scale_log2 > kGrow;
         if (__any_sync(0xffffffffu, grow)) {
           const float now = grow ? top : m;
@@ -242,25 +254,36 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_mma_kernel(const __grid_co
           }
         }
         const float ms = m * a.scale_log2;
-        float s0 = 0.f, s1 = 0.f;
+        const uint64_t sc = pair(a.scale_log2, a.scale_log2), off = pair(-ms, -ms);
+        uint64_t s0 = 0, s1 = 0;                 // pairs of zeros
 #pragma unroll
-        for (int c = 0; c < 128; c += 32) {
+        for (int c = 0; c < 4; ++c) {
           uint32_t pk[16];
 #pragma unroll
-          for (int e = 0; e < 32; e += 2) {
-            const float p0 = exp2_fast(fmaf(x[c + e], a.scale_log2, -ms));
-            const float p1 = exp2_fast(fmaf(x[c + e + 1], a.scale_log2, -ms));
-            s0 += p0;
-            s1 += p1;
-            pk[e / 2] = pack_bf16(p0, p1);
+          for (int e = 0; e < 16; ++e) {
+            const uint64_t y = fma2(pair(x[32 * c + 2 * e], x[32 * c + 2 * e + 1]), sc, off);
+            float2 p;
+            if (e % 16 % 3 == kPolyAt) {
+              p = exp2_poly(y);
+            } else {
+              const float2 v = unpair(y);
+              p = make_float2(exp2_fast(v.x), exp2_fast(v.y));
+            }
+            if (e & 1) s1 = add2(s1, pair(p.x, p.y));
+            else s0 = add2(s0, pair(p.x, p.y));
+            pk[e] = pack_bf16(p.x, p.y);
           }
-          tmem_st<16>(s_tm + c / 2, pk);
+          tmem_st<16>(s_tm + 16 * c, pk);
+          if (c & 1) {
+            // half of the weights are there: their products can start
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sm.p_full[q][c >> 1]);
+          }
         }
-        l += s0 + s1;
-        tmem_wait_st();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sm.p_full[q]);
+        const float2 sum = unpair(add2(s0, s1));
+        l += sum.x + sum.y;
       }
       if (!ok) break;
       if (first >= u.nq) continue;
@@ -270,6 +293,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_mma_kernel(const __grid_co
         ++outs;
         tc_fence_after();
       }
+      if (lim <= 0) l = 0.f;                     // nothing to attend
       const float inv = l > 0.f ? 1.f / l : 0.f;
       const int64_t row = static_cast<int64_t>(u.q0 + i) * a.H + u.h;
       for (int c = 0; c < a.d_v; c += 32) {
@@ -357,19 +381,22 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_mma_kernel(const __grid_co
           umma_commit(&sm.s_full[q]);
           return true;
         };
-        // O_q of the next V part
+        // O_q of the next V part, in two halves of the keys as their weights come
         auto values = [&](int q, bool first, bool final, bool last) {
           if (first && outs[q] > 0 && !bounded_wait(&sm.o_empty[q], (outs[q] - 1) & 1u, wc)) return false;
           if (!v_here && !bounded_wait(&sm.full[vp % kParts], (vp / kParts) & 1u, wc)) return false;
           v_here = true;
-          if (!bounded_wait(&sm.p_full[q], ptile[q] & 1u, wc)) return false;
-          ++ptile[q];
-          tc_fence_after();
-          int s = vc;
-          for (int j = 0; j < a.v_blocks; ++j) {
-            umma_ts_steps<8, 128>(tmem + 256 + q * 128 + j * 64, tmem + q * 128, r0 + s * kBlockStep, id_o, first ? 0u : 1u);
-            if (++s == a.ring) s = 0;
+          for (int half = 0; half < 2; ++half) {
+            if (!bounded_wait(&sm.p_full[q][half], ptile[q] & 1u, wc)) return false;
+            tc_fence_after();
+            int s = vc;
+            for (int j = 0; j < a.v_blocks; ++j) {
+              umma_ts_steps<4, 128>(tmem + 256 + q * 128 + j * 64, tmem + q * 128 + half * 32, r0 + s * kBlockStep + half * 512, id_o,
+                                    first && half == 0 ? 0u : 1u);
+              if (++s == a.ring) s = 0;
+            }
           }
+          ++ptile[q];
           if (last) {
             umma_commit(&sm.empty[vp % kParts]);
             advance(vc, vp);
@@ -381,14 +408,12 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_mma_kernel(const __grid_co
           }
           return true;
         };
-        if (n0 > 0) ok = scores(0, n1 == 0);
-        if (ok && n1 > 0) ok = scores(1, true);
-        if (ok && nt == 1) umma_commit(&sm.q_empty);
-        for (int t = 0; t < nt && ok; ++t) {
-          if (t < n0) ok = values(0, t == 0, t == n0 - 1, t >= n1);
-          if (ok && t + 1 < n0) ok = scores(0, t + 1 >= n1);
-          if (ok && t < n1) ok = values(1, t == 0, t == n1 - 1, true);
-          if (ok && t + 1 < n1) ok = scores(1, true);
+        for (int t = -1; t < nt && ok; ++t) {
+          for (int q = 0; q < 2 && ok; ++q) {
+            const int n = q == 0 ? n0 : n1;
+            if (t >= 0 && t < n) ok = values(q, t == 0, t == n - 1, q == 1 || t >= n1);
+            if (ok && t + 1 < n) ok = scores(q, q == 1 || t + 1 >= n1);
+          }
           if (ok && t + 2 == nt) umma_commit(&sm.q_empty);
         }
       }
