@@ -42,7 +42,7 @@ li_status check_attn_ws(li_ctx* c, const void* ws, size_t bytes, size_t need, co
 }
 
 // Checks a row transform for rows of `dim` elements; *chunked tells whether
-// its ranges suit the wide path (whole chunks of 8, partners in reach).
+// its ranges suit the wide path (whole chunks of 8).
 li_status check_transform(li_ctx* c, const li_row_transform& tf, int dim, bool* chunked, const char* what) {
   if (tf.norm != LI_NORM_NONE && tf.norm != LI_NORM_RMS && tf.norm != LI_NORM_LAYER)
     return fail(c, LI_ERR_ARG, "%s: unknown norm %d", what, static_cast<int>(tf.norm));
@@ -61,7 +61,7 @@ li_status check_transform(li_ctx* c, const li_row_transform& tf, int dim, bool* 
     if (!tf.inv_freq) return fail(c, LI_ERR_ARG, "%s: inv_freq is NULL", what);
     if (!aligned(tf.inv_freq, 4)) return fail(c, LI_ERR_ALIGN, "%s: inv_freq must be 4-byte aligned", what);
     if (tf.rope_offset % 8 || tf.rope_dim % 8) *chunked = false;
-    if (tf.rope_halves && (tf.rope_dim % 16 || dim > 256)) *chunked = false;
+    if (tf.rope_halves && tf.rope_dim % 16) *chunked = false;
   }
   return LI_OK;
 }
@@ -113,30 +113,26 @@ li_status norm_rope(li_ctx* c, const li_head_rows* sets, int n_sets, li_dtype dt
     heads += r.H;
     a.set[i] = r;
   }
-  // the partner chunk of a rotation by halves has to be in another lane, so
-  // one wide set past 256 elements decides for all of them
-  if (max_dim > 256)
-    for (int i = 0; i < n_sets; ++i)
-      if (sets[i].tf.rope_dim && sets[i].tf.rope_halves) vec = false;
   if (pos && !aligned(pos, 4)) return fail(c, LI_ERR_ALIGN, "%s: pos must be 4-byte aligned", what);
   if (heads > 65535) return fail(c, LI_ERR_SHAPE, "%s: more than 65535 heads", what);
   if (n_tok == 0) return LI_OK;
   a.n_sets = n_sets;
-  a.heads = static_cast<int>(heads);
-  a.n_tok = n_tok;
   a.pos = pos;
-  // A block takes all heads of a token (its angles once) when the tokens
-  // alone fill the GPU, else as few as one pass of its lanes covers.
-  const int lanes = max_dim <= 64 ? 8 : (max_dim <= 128 ? 16 : 32);
-  const int per_pass = vec ? 256 / lanes : 4;
-  a.heads_per_block = a.heads;
-  if (n_tok < 4 * c->num_sms) a.heads_per_block = std::min(a.heads, per_pass);
-  const int64_t grid = n_tok * ((a.heads + a.heads_per_block - 1) / a.heads_per_block);
+  const NormRopePlan plan = plan_norm_rope(sets, n_sets, vec, max_dim);
+  for (int i = 0; i < n_sets; ++i) {
+    a.tasks += (sets[i].H + plan.rows - 1) / plan.rows;
+    a.tab_stride = std::max(a.tab_stride, (sets[i].tf.rope_dim / 2 + 1) / 2 * 2);
+  }
+  // A block takes all of a token's tasks (its angles once) when the tokens
+  // alone fill the GPU, else one a warp.
+  a.per_block = n_tok < 4 * c->num_sms ? std::min(a.tasks, plan.warps) : a.tasks;
+  a.blocks = (a.tasks + a.per_block - 1) / a.per_block;
+  const int64_t grid = n_tok * a.blocks;
   if (grid >= (int64_t(1) << 31)) return fail(c, LI_ERR_SHAPE, "%s: too many tokens (%lld)", what, static_cast<long long>(n_tok));
   if ((s = check_device(c, what)) != LI_OK) return s;
   (void)cudaGetLastError();
-  Launch L(c, st, "norm_rope", static_cast<int>(grid), vec ? 256 : 128, 0);
-  const cudaError_t e = launch_norm_rope(a, dtype, vec, max_dim, grid, st);
+  Launch L(c, st, "norm_rope", static_cast<int>(grid), plan.lanes ? 256 : 128, 0);
+  const cudaError_t e = launch_norm_rope(a, dtype, plan, grid, st);
   L.done();
   return e == cudaSuccess ? LI_OK : cuda_fail(c, e, "norm_rope launch");
 }
@@ -161,6 +157,7 @@ li_status append_paged(li_ctx* c, const li_paged_cache* cache, const void* x, in
     if ((s = check_transform(c, *tf, cache->dim, &vec, what)) != LI_OK) return s;
     a.tf = *tf;
   }
+  vec = vec && append_in_chunks(a.tf, cache->dim);
   if ((s = check_attn_ws(c, ws, ws_bytes, kAttnHeader, what)) != LI_OK) return s;
   if ((s = check_device(c, what)) != LI_OK) return s;
   a.x = x;
@@ -269,13 +266,13 @@ li_status latent_attention(li_ctx* c, const li_paged_cache* cache, const void* q
     return latent_mma(c, cache, q, T, H, d_v, scale, q_pos, sel, k, out, lse, ws, st);
   LatentAttnArgs a;
   memset(&a, 0, sizeof(a));
-  a.q = q;
-  a.data = cache->data;
+  a.q = static_cast<const float*>(q);
+  a.data = static_cast<const float*>(cache->data);
   a.page_table = cache->page_table;
   a.lengths = cache->lengths;
   a.q_pos = q_pos;
   a.sel = sel;
-  a.out = out;
+  a.out = static_cast<float*>(out);
   a.lse = lse;
   a.status = at<int>(ws, 0);
   a.batch = cache->batch;
@@ -290,7 +287,7 @@ li_status latent_attention(li_ctx* c, const li_paged_cache* cache, const void* q
   a.scale = scale;
   (void)cudaGetLastError();
   Launch L(c, st, "latent_attn_rows", 0, 256, 0);
-  const cudaError_t e = launch_latent_attn_rows(a, cache->dtype, st);
+  const cudaError_t e = launch_latent_attn_rows(a, st);
   L.done();
   return e == cudaSuccess ? LI_OK : cuda_fail(c, e, "latent attention launch");
 }
@@ -347,7 +344,7 @@ li_status prompt_mma(li_ctx* c, const li_prompt& p, void* out, float* lse, void*
   }
   if (s != LI_OK) return s;
   (void)cudaGetLastError();
-  Launch L(c, st, "prompt_attn", a.grid, 352, static_cast<int>(a.smem_bytes));
+  Launch L(c, st, "prompt_attn", a.grid, 608, static_cast<int>(a.smem_bytes));
   const cudaError_t e = launch_prompt_mma(a, st);
   L.done();
   return e == cudaSuccess ? LI_OK : cuda_fail(c, e, "prompt attention launch");
@@ -389,7 +386,7 @@ li_status prompt_attention(li_ctx* c, const li_prompt* p, void* out, float* lse,
   if (p->dtype == LI_BF16) return prompt_mma(c, a, out, lse, ws, st);
   (void)cudaGetLastError();
   Launch L(c, st, "prompt_attn_rows", 0, 256, 0);
-  const cudaError_t e = launch_prompt_attn_rows(a, out, lse, st);
+  const cudaError_t e = launch_prompt_attn_rows(a, static_cast<float*>(out), lse, st);
   L.done();
   return e == cudaSuccess ? LI_OK : cuda_fail(c, e, "prompt attention launch");
 }

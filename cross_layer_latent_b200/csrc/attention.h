@@ -17,9 +17,9 @@ constexpr int kMaxRowDim = 1024;
 struct NormRopeArgs {
   li_head_rows set[kMaxRowSets];
   int n_sets;
-  int heads;               // heads of all sets together
-  int heads_per_block;
-  int64_t n_tok;
+  int tasks;               // of a token: a warp's worth of rows of one set each
+  int per_block, blocks;   // tasks of a block, blocks of a token
+  int tab_stride;          // slots of a set's table of angles (even)
   const int32_t* pos;
 };
 
@@ -37,19 +37,27 @@ struct AppendPagedArgs {
   int* status;
 };
 
-cudaError_t launch_norm_rope(const NormRopeArgs& a, li_dtype dtype, bool vec, int max_dim, int64_t grid, cudaStream_t st);
+// How the rows are spread: lanes a row (0: a warp by way of shared memory) in
+// chunks of 8 elements, rows of a warp's task, warps of a block.
+struct NormRopePlan {
+  int lanes, chunks, rows, warps;
+  bool plain;              // RMS or no norm, no beta, rotary chunks in one register row
+};
+NormRopePlan plan_norm_rope(const li_head_rows* sets, int n_sets, bool chunked, int max_dim);
+bool append_in_chunks(const li_row_transform& tf, int dim);
+cudaError_t launch_norm_rope(const NormRopeArgs& a, li_dtype dtype, const NormRopePlan& p, int64_t grid, cudaStream_t st);
 cudaError_t launch_append_paged(const AppendPagedArgs& a, li_dtype dtype, bool vec, int num_sms, cudaStream_t st);
 
 // ---- attention
 
 struct LatentAttnArgs {
-  const void* q;
-  const void* data;
+  const float* q;
+  const float* data;
   const int32_t* page_table;
   const int32_t* lengths;
   const int32_t* q_pos;
   const int32_t* sel;
-  void* out;
+  float* out;
   float* lse;
   int* status;
   int batch, T, H, k, dim, d_v;
@@ -127,7 +135,8 @@ struct alignas(64) PromptMmaArgs {
 bool prompt_mma_layout(PromptMmaArgs* a, int num_sms, int max_smem);
 cudaError_t launch_prompt_mma(const PromptMmaArgs& a, cudaStream_t st);
 
-cudaError_t launch_latent_attn_rows(const LatentAttnArgs& a, li_dtype dtype, cudaStream_t st);
-cudaError_t launch_prompt_attn_rows(const li_prompt& p, void* out, float* lse, cudaStream_t st);
+// fp32 (attn_rows.cu).
+cudaError_t launch_latent_attn_rows(const LatentAttnArgs& a, cudaStream_t st);
+cudaError_t launch_prompt_attn_rows(const li_prompt& p, float* out, float* lse, cudaStream_t st);
 
 }  // namespace li

@@ -38,12 +38,12 @@ namespace {
 constexpr int kTile = 128;
 constexpr int kRows = 2 * kTile;                 // queries of a unit
 constexpr int kBlockBytes = kTile * 128;
-constexpr int kSoftWarps = 8;                    // a warpgroup for each query tile
-constexpr int kMmaWarp = 8, kLoadWarp = 9;   // and one that zeroes
-constexpr int kThreads = 32 * 11;
+constexpr int kSoftWarps = 16;                   // two warpgroups for each query tile, half of the keys each
+constexpr int kMmaWarp = 16, kLoadWarp = 17;     // and one that zeroes
+constexpr int kThreads = 32 * 19;
 constexpr int kMaxRing = 13;
 constexpr int kParts = 8;                        // parts in flight at most (a power of two)
-constexpr int kPolyAt = 2;                       // of every three pairs of exponentials one is computed on the FMA pipes
+constexpr int kPolyOf = 4;                       // of so many pairs of exponentials one is computed on the FMA pipes
 constexpr float kGrow = 8.f;
 constexpr float kNoMax = -1e30f;
 constexpr uint64_t kDrainNs = 1000ull * 1000ull;
@@ -57,8 +57,9 @@ struct Unit {
 struct Smem {
   uint64_t full[kParts], empty[kParts], raw[kParts];
   uint64_t unit_full[2], unit_empty[2];
-  uint64_t q_full, q_empty, s_full[2], p_full[2][2], o_full[2], o_empty[2], drain;
+  uint64_t q_full, q_empty, s_full[2], p_full[2], o_full[2], o_empty[2], drain;
   Unit unit[2];
+  float part[2][2][kTile];                       // by query tile, half of the keys and row
   uint32_t tmem;
   int abort_flag;
 };
@@ -149,10 +150,9 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_mma_kernel(const __grid_co
       mbar_init(&sm.unit_full[i], 1);
       mbar_init(&sm.unit_empty[i], kSoftWarps + 2);
       mbar_init(&sm.s_full[i], 1);
-      mbar_init(&sm.p_full[i][0], 4);
-      mbar_init(&sm.p_full[i][1], 4);
+      mbar_init(&sm.p_full[i], 8);
       mbar_init(&sm.o_full[i], 1);
-      mbar_init(&sm.o_empty[i], 4);
+      mbar_init(&sm.o_empty[i], 8);
     }
     mbar_init(&sm.q_full, 1);
     mbar_init(&sm.q_empty, 1);
@@ -177,14 +177,19 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_mma_kernel(const __grid_co
 
   if (warp < kSoftWarps) {
     // ------------------------------------------------ softmax and output of query tile q
-    const int q = warp >> 2, quad = warp & 3;
+    // A row has two threads, one for 64 of a tile's keys: with 128 keys a thread, a warp alone on its scheduler
+    // took 2100 cycles a tile, most of them waiting for its own results.
+    const int q = warp >> 3, half = (warp >> 2) & 1, quad = warp & 3;
     const uint32_t lanes = static_cast<uint32_t>(quad * 32) << 16;
     const uint32_t s_tm = tmem + q * 128 + lanes, o_tm = tmem + 256 + q * 128 + lanes;
     const int r = quad * 32 + lane;
+    const int bar = 1 + q;
+    const int my_cols = a.v_blocks * 32;         // output columns of a half
     uint32_t tile = 0, outs = 0;
     bool ok = true;
     for (uint32_t un = 0; ok; ++un) {
-      ok = __all_sync(0xffffffffu, bounded_wait_sleep(&sm.unit_full[un & 1], (un >> 1) & 1u, wc));
+      ok = bounded_wait_sleep(&sm.unit_full[un & 1], (un >> 1) & 1u, wc);
+      ok = !named_bar_any(bar, 256, !ok);
       if (!ok) break;
       const Unit u = sm.unit[un & 1];
       __syncwarp();
@@ -196,60 +201,59 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_mma_kernel(const __grid_co
       const int lim = i < u.nq ? key_limit(a, u, i) : u.nk;
       float m = kNoMax, l = 0.f;
       for (int t = 0; t < n; ++t, ++tile) {
-        ok = __all_sync(0xffffffffu, bounded_wait(&sm.s_full[q], tile & 1u, wc));
-        if (!ok) break;
+        ok = bounded_wait(&sm.s_full[q], tile & 1u, wc);
+        __syncwarp();
         tc_fence_after();
-        float x[128];
-        const int left = lim - t * kTile;
-        const bool mask = __any_sync(0xffffffffu, left < kTile);
-        float top4[4];
-        uint32_t xr[2][32];
-        tmem_ld<32>(s_tm, xr[0]);
-        tmem_wait_ld();
+        float x[64];
+        {
+          uint32_t xr[2][32];
+          tmem_ld<32>(s_tm + 64 * half, xr[0]);
+          tmem_ld<32>(s_tm + 64 * half + 32, xr[1]);
+          tmem_wait_ld();
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          // a quarter's maximum while the next quarter is on its way
-          if (c < 3) tmem_ld<32>(s_tm + 32 * (c + 1), xr[(c + 1) & 1]);
-#pragma unroll
-          for (int e = 0; e < 32; ++e) {
-            x[32 * c + e] = __uint_as_float(xr[c & 1][e]);
-            if (a.negate) x[32 * c + e] = -x[32 * c + e];
-          }
-          if (mask) {
-#pragma unroll
-            for (int e = 0; e < 32; ++e)
-              if (32 * c + e >= left) x[32 * c + e] = -INFINITY;
-          }
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            if (c == 0) top4[e] = x[e];
-            else top4[e] = fmaxf(top4[e], x[32 * c + e]);
-          }
-#pragma unroll
-          for (int i = 4; i < 28; i += 8)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) top4[e] = fmaxf(fmaxf(top4[e], x[32 * c + i + e]), x[32 * c + i + 4 + e]);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) top4[e] = fmaxf(top4[e], x[32 * c + 28 + e]);
-          if (c < 3) tmem_wait_ld();
+          for (int c = 0; c < 64; ++c) x[c] = __uint_as_float(xr[c / 32][c % 32]);
         }
-        const float top = fmaxf(fmaxf(top4[0], top4[1]), fmaxf(top4[2], top4[3]));
-        const bool grow = (top - m) * a.scale_log2 > kGrow;
-        if (__any_sync(0xffffffffu, grow)) {
-          const float now = grow ? top : m;
-          const float keep = exp2_fast((m - now) * a.scale_log2);
-          m = now;
-          l *= keep;
-          if (t > 0) {
-            // the previous tile's product is complete: s_full was committed after it
-#pragma unroll 1
-            for (int c = 0; c < a.v_blocks * 64; c += 16) {
-              uint32_t o[16];
-              tmem_ld<16>(o_tm + c, o);
-              tmem_wait_ld();
+        if (a.negate) {
 #pragma unroll
-              for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * keep);
-              tmem_st<16>(o_tm + c, o);
+          for (int c = 0; c < 64; ++c) x[c] = -x[c];
+        }
+        const int left = lim - t * kTile - 64 * half;
+        if (__any_sync(0xffffffffu, left < 64)) {
+#pragma unroll
+          for (int c = 0; c < 64; ++c)
+            if (c >= left) x[c] = -INFINITY;
+        }
+        float top4[4] = {x[0], x[1], x[2], x[3]};
+#pragma unroll
+        for (int c = 4; c < 60; c += 8)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) top4[e] = fmaxf(fmaxf(top4[e], x[c + e]), x[c + 4 + e]);
+        float top = fmaxf(fmaxf(fmaxf(top4[0], x[60]), fmaxf(top4[1], x[61])), fmaxf(fmaxf(top4[2], x[62]), fmaxf(top4[3], x[63])));
+        // every score of the tile has been read when this returns
+        if (named_bar_any(bar, 256, (top - m) * a.scale_log2 > kGrow || !ok)) {
+          sm.part[q][half][r] = top;
+          if (named_bar_any(bar, 256, !ok)) {
+            ok = false;
+            break;
+          }
+          top = fmaxf(top, sm.part[q][half ^ 1][r]);
+          const bool grow = (top - m) * a.scale_log2 > kGrow;
+          if (__any_sync(0xffffffffu, grow)) {
+            const float now = grow ? top : m;
+            const float keep = exp2_fast((m - now) * a.scale_log2);
+            m = now;
+            l *= keep;
+            if (t > 0) {
+              // the previous tile's product is complete: s_full was committed after it
+#pragma unroll 1
+              for (int c = half * my_cols; c < (half + 1) * my_cols; c += 16) {
+                uint32_t o[16];
+                tmem_ld<16>(o_tm + c, o);
+                tmem_wait_ld();
+#pragma unroll
+                for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * keep);
+                tmem_st<16>(o_tm + c, o);
+              }
             }
           }
         }
@@ -257,13 +261,13 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_mma_kernel(const __grid_co
         const uint64_t sc = pair(a.scale_log2, a.scale_log2), off = pair(-ms, -ms);
         uint64_t s0 = 0, s1 = 0;                 // pairs of zeros
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
+        for (int c = 0; c < 2; ++c) {
           uint32_t pk[16];
 #pragma unroll
           for (int e = 0; e < 16; ++e) {
             const uint64_t y = fma2(pair(x[32 * c + 2 * e], x[32 * c + 2 * e + 1]), sc, off);
             float2 p;
-            if (e % 16 % 3 == kPolyAt) {
+            if (e % kPolyOf == kPolyOf - 1) {
               p = exp2_poly(y);
             } else {
               const float2 v = unpair(y);
@@ -273,30 +277,31 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_mma_kernel(const __grid_co
             else s0 = add2(s0, pair(p.x, p.y));
             pk[e] = pack_bf16(p.x, p.y);
           }
-          tmem_st<16>(s_tm + 16 * c, pk);
-          if (c & 1) {
-            // half of the weights are there: their products can start
-            tmem_wait_st();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&sm.p_full[q][c >> 1]);
-          }
+          tmem_st<16>(s_tm + 32 * half + 16 * c, pk);
         }
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.p_full[q]);
         const float2 sum = unpair(add2(s0, s1));
         l += sum.x + sum.y;
       }
       if (!ok) break;
       if (first >= u.nq) continue;
-      if (n > 0) {
-        ok = __all_sync(0xffffffffu, bounded_wait(&sm.o_full[q], outs & 1u, wc));
-        if (!ok) break;
-        ++outs;
-        tc_fence_after();
-      }
+      // the row's sum: both halves, after the last tile's maxima have been read
       if (lim <= 0) l = 0.f;                     // nothing to attend
+      named_bar_sync(bar, 256);
+      sm.part[q][half][r] = l;
+      ok = n == 0 || bounded_wait(&sm.o_full[q], outs & 1u, wc);
+      if (named_bar_any(bar, 256, !ok)) {
+        ok = false;
+        break;
+      }
+      l += sm.part[q][half ^ 1][r];
+      tc_fence_after();
       const float inv = l > 0.f ? 1.f / l : 0.f;
       const int64_t row = static_cast<int64_t>(u.q0 + i) * a.H + u.h;
-      for (int c = 0; c < a.d_v; c += 32) {
+      for (int c = half * my_cols; c < min((half + 1) * my_cols, a.d_v); c += 32) {
         uint32_t o[32];
         if (n > 0) {
           tmem_ld<32>(o_tm + c, o);
@@ -320,8 +325,9 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_mma_kernel(const __grid_co
           }
         }
       }
-      if (a.lse && i < u.nq) a.lse[row] = l > 0.f ? (m * a.scale_log2 + log2f(l)) * 0.69314718056f : -INFINITY;
+      if (a.lse && half == 0 && i < u.nq) a.lse[row] = l > 0.f ? (m * a.scale_log2 + log2f(l)) * 0.69314718056f : -INFINITY;
       if (n > 0) {
+        ++outs;
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&sm.o_empty[q]);
@@ -332,7 +338,8 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_mma_kernel(const __grid_co
     if (elect_one()) {
       const uint32_t id_s = make_instr_desc(1, 128, 128);
       const uint32_t id_o = make_instr_desc(1, 128, 64) | kMajorMnB;
-      const uint32_t q0 = desc_lo(smem_addr(base), 0), r0 = desc_lo(smem_addr(ring), 0);
+      const uint32_t id_o2 = make_instr_desc(1, 128, 128) | kMajorMnB;
+      const uint32_t q0 = desc_lo(smem_addr(base), 0), r0 = desc_lo(smem_addr(ring), 0), v0 = desc_lo(smem_addr(ring), kBlockBytes);
       constexpr uint32_t kBlockStep = kBlockBytes >> 4;
       const int per = nkb + a.v_blocks;
       int kc = 0, vc = nkb;                      // ring positions of the next K part and V part
@@ -381,22 +388,24 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_mma_kernel(const __grid_co
           umma_commit(&sm.s_full[q]);
           return true;
         };
-        // O_q of the next V part, in two halves of the keys as their weights come
+        // O_q of the next V part
         auto values = [&](int q, bool first, bool final, bool last) {
           if (first && outs[q] > 0 && !bounded_wait(&sm.o_empty[q], (outs[q] - 1) & 1u, wc)) return false;
           if (!v_here && !bounded_wait(&sm.full[vp % kParts], (vp / kParts) & 1u, wc)) return false;
           v_here = true;
-          for (int half = 0; half < 2; ++half) {
-            if (!bounded_wait(&sm.p_full[q][half], ptile[q] & 1u, wc)) return false;
-            tc_fence_after();
+          if (!bounded_wait(&sm.p_full[q], ptile[q] & 1u, wc)) return false;
+          ++ptile[q];
+          tc_fence_after();
+          if (a.v_blocks == 2 && vc + 1 < a.ring) {
+            // both blocks side by side: one MMA takes 128 columns
+            umma_ts_steps<8, 128>(tmem + 256 + q * 128, tmem + q * 128, v0 + vc * kBlockStep, id_o2, first ? 0u : 1u);
+          } else {
             int s = vc;
             for (int j = 0; j < a.v_blocks; ++j) {
-              umma_ts_steps<4, 128>(tmem + 256 + q * 128 + j * 64, tmem + q * 128 + half * 32, r0 + s * kBlockStep + half * 512, id_o,
-                                    first && half == 0 ? 0u : 1u);
+              umma_ts_steps<8, 128>(tmem + 256 + q * 128 + j * 64, tmem + q * 128, v0 + s * kBlockStep, id_o, first ? 0u : 1u);
               if (++s == a.ring) s = 0;
             }
           }
-          ++ptile[q];
           if (last) {
             umma_commit(&sm.empty[vp % kParts]);
             advance(vc, vp);

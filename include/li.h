@@ -413,7 +413,9 @@ typedef enum { LI_NORM_NONE = 0, LI_NORM_RMS = 1, LI_NORM_LAYER = 2 } li_norm;
  *   [rope_dim / 2] fp32, device): x' = x cos - y sin, y' = x sin + y cos.
  *   Slot p is (x[2p], x[2p+1]) with rope_halves = 0, the layout of
  *   li_append_latent_ex, and (x[p], x[p + rope_dim / 2]) with rope_halves = 1.
- *   The angle is formed and reduced to a turn in double precision.
+ *   The angle is formed exactly, modulo whole turns, before its cosine and
+ *   sine are taken in fp32 (for BF16 rows to 2^-20).  Frequencies must be
+ *   finite.
  * norm = LI_NORM_NONE and rope_dim = 0 switch the parts off.                */
 typedef struct {
   li_norm norm;
