@@ -292,21 +292,21 @@ li_status latent_attention(li_ctx* c, const li_paged_cache* cache, const void* q
   return e == cudaSuccess ? LI_OK : cuda_fail(c, e, "latent attention launch");
 }
 
-// A tensor of rows [tokens][heads][d] as a map with 128-row boxes of 64
+// A tensor of rows [tokens][heads][d] as a map with boxes of `rows` rows and 64
 // columns (heads = 0: no head dimension).  Strides of dimensions of one
 // element are free, so they are set to something the map takes.
-li_status rows_map(li_ctx* c, CUtensorMap* m, const void* base, int d, int heads, int tokens, int64_t head_stride,
+li_status rows_map(li_ctx* c, CUtensorMap* m, const void* base, int rows, int d, int heads, int tokens, int64_t head_stride,
                    int64_t tok_stride) {
   const cuuint64_t hs = static_cast<cuuint64_t>(heads > 1 ? head_stride : (d + 7) / 8 * 8) * 2;
   const cuuint64_t ts = static_cast<cuuint64_t>(tokens > 1 ? tok_stride : (d + 7) / 8 * 8) * 2;
   if (heads == 0) {
     const cuuint64_t dims[2] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(tokens)}, str[1] = {ts};
-    const cuuint32_t box[2] = {64, 128};
+    const cuuint32_t box[2] = {64, static_cast<cuuint32_t>(rows)};
     return encode_map(c, m, LI_BF16, 2, const_cast<void*>(base), dims, str, box, 128);
   }
   const cuuint64_t dims[3] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(heads), static_cast<cuuint64_t>(tokens)};
   const cuuint64_t str[2] = {hs, ts};
-  const cuuint32_t box[3] = {64, 1, 128};
+  const cuuint32_t box[3] = {64, 1, static_cast<cuuint32_t>(rows)};
   return encode_map(c, m, LI_BF16, 3, const_cast<void*>(base), dims, str, box, 128);
 }
 
@@ -336,11 +336,11 @@ li_status prompt_mma(li_ctx* c, const li_prompt& p, void* out, float* lse, void*
   a.d_v = p.d_v;
   if (!prompt_mma_layout(&a, c->num_sms, c->max_smem_optin))
     return fail(c, LI_ERR_UNSUPPORTED, "%s: operands too large for shared memory", what);
-  li_status s = rows_map(c, &a.map_q, p.q, p.d_nope + p.d_rope, p.H, p.total_q, p.q_head_stride, p.q_tok_stride);
+  li_status s = rows_map(c, &a.map_q, p.q, 128, p.d_nope + p.d_rope, p.H, p.total_q, p.q_head_stride, p.q_tok_stride);
   if (s == LI_OK && p.total_k > 0) {
-    s = rows_map(c, &a.map_k, p.k_nope, p.d_nope, p.H, p.total_k, p.k_head_stride, p.k_tok_stride);
-    if (s == LI_OK) s = rows_map(c, &a.map_v, p.v, p.d_v, p.H, p.total_k, p.v_head_stride, p.v_tok_stride);
-    if (s == LI_OK && p.d_rope) s = rows_map(c, &a.map_kr, p.k_rope, p.d_rope, 0, p.total_k, 0, p.kr_tok_stride);
+    s = rows_map(c, &a.map_k, p.k_nope, 64, p.d_nope, p.H, p.total_k, p.k_head_stride, p.k_tok_stride);
+    if (s == LI_OK) s = rows_map(c, &a.map_v, p.v, 64, p.d_v, p.H, p.total_k, p.v_head_stride, p.v_tok_stride);
+    if (s == LI_OK && p.d_rope) s = rows_map(c, &a.map_kr, p.k_rope, 64, p.d_rope, 0, p.total_k, 0, p.kr_tok_stride);
   }
   if (s != LI_OK) return s;
   (void)cudaGetLastError();
