@@ -326,6 +326,7 @@ li_status prompt_mma(li_ctx* c, const li_prompt& p, void* out, float* lse, void*
   a.scale_log2 = std::max(std::fabs(p.scale) * 1.44269504089f, 1e-30f);
   a.negate = p.scale < 0.f;
   a.causal = p.causal != 0;
+  a.wide_out = aligned(out, 32) && p.d_v % 16 == 0;
   a.batch = p.batch;
   a.H = p.H;
   a.total_q = p.total_q;
@@ -344,7 +345,7 @@ li_status prompt_mma(li_ctx* c, const li_prompt& p, void* out, float* lse, void*
   }
   if (s != LI_OK) return s;
   (void)cudaGetLastError();
-  Launch L(c, st, "prompt_attn", a.grid, 608, static_cast<int>(a.smem_bytes));
+  Launch L(c, st, "prompt_attn", a.grid, 640, static_cast<int>(a.smem_bytes));
   const cudaError_t e = launch_prompt_mma(a, st);
   L.done();
   return e == cudaSuccess ? LI_OK : cuda_fail(c, e, "prompt attention launch");

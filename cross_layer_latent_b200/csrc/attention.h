@@ -122,6 +122,7 @@ struct alignas(64) PromptMmaArgs {
   float scale_log2;       // |scale| * log2(e)
   int negate;             // scale < 0
   int causal;
+  int wide_out;           // every output row is 32-byte aligned
   int batch, H, total_q, total_k, max_q;
   int d_nope, d_rope, d_v;
   // filled by prompt_mma_layout

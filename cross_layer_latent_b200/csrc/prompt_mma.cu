@@ -46,8 +46,8 @@ constexpr int kQBlockBytes = kTile * 128;        // 128 rows x 64 bf16
 constexpr int kBlockBytes = 64 * 128;            // 64 rows x 64 bf16
 constexpr int kVBlocks = 2;                      // blocks of a V part: 128 keys x 64 columns
 constexpr int kSoftWarps = 16;                   // two warpgroups for each query tile, half of the keys each
-constexpr int kMmaWarp = 16, kLoadWarp = 17;     // and one that zeroes
-constexpr int kThreads = 32 * 19;
+constexpr int kMmaWarp = 16, kLoadWarp = 17, kUnitWarp = 18;   // and one that zeroes
+constexpr int kThreads = 32 * 20;
 constexpr int kMaxRing = 24;
 constexpr int kParts = 8;                        // parts in flight at most (a power of two)
 constexpr int kPolyOf = 4;                       // of so many pairs of exponentials one is computed on the FMA pipes
@@ -139,6 +139,13 @@ __device__ __forceinline__ Unit find_unit(const PromptMmaArgs& a, int64_t x, int
   return u;
 }
 
+// 32 bytes in one store (p 32-byte aligned).
+__device__ __forceinline__ void st_global_32(void* p, const uint32_t* w) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]),
+               "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+               : "memory");
+}
+
 __global__ void __launch_bounds__(kThreads, 1) prompt_mma_kernel(const __grid_constant__ PromptMmaArgs a) {
   extern __shared__ uint8_t raw_smem[];
   uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw_smem) + 1023) & ~uintptr_t(1023));
@@ -157,7 +164,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_mma_kernel(const __grid_co
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sm.unit_full[i], 1);
-      mbar_init(&sm.unit_empty[i], 2 * kSoftWarps + 4);   // softmax, MMA issue or loads, and zeroes of both CTAs
+      mbar_init(&sm.unit_empty[i], 2 * kSoftWarps + 5);   // MMA issue, and softmax, loads and zeroes of both CTAs
       mbar_init(&sm.s_full[i], 1);
       mbar_init(&sm.p_full[i], 16);
       mbar_init(&sm.o_full[i], 1);
@@ -320,17 +327,19 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_mma_kernel(const __grid_co
           for (int e = 0; e < 32; ++e) o[e] = 0u;
         }
         if (i < u.nq) {
-          uint4* out = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + row * a.d_v + c);
+          __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out) + row * a.d_v + c;
+          uint32_t w[16];
 #pragma unroll
-          for (int e = 0; e < 32; e += 8) {
-            if (c + e < a.d_v) {
-              uint4 w;
-              w.x = pack_bf16(__uint_as_float(o[e]) * inv, __uint_as_float(o[e + 1]) * inv);
-              w.y = pack_bf16(__uint_as_float(o[e + 2]) * inv, __uint_as_float(o[e + 3]) * inv);
-              w.z = pack_bf16(__uint_as_float(o[e + 4]) * inv, __uint_as_float(o[e + 5]) * inv);
-              w.w = pack_bf16(__uint_as_float(o[e + 6]) * inv, __uint_as_float(o[e + 7]) * inv);
-              out[e / 8] = w;
-            }
+          for (int e = 0; e < 16; ++e) w[e] = pack_bf16(__uint_as_float(o[2 * e]) * inv, __uint_as_float(o[2 * e + 1]) * inv);
+          // rows lie apart, so a store takes as many cycles as it has rows: 32 bytes a thread where they are aligned
+          if (a.wide_out) {
+#pragma unroll
+            for (int e = 0; e < 16; e += 8)
+              if (c + 2 * e < a.d_v) st_global_32(out + 2 * e, &w[e]);
+          } else {
+#pragma unroll
+            for (int e = 0; e < 16; e += 4)
+              if (c + 2 * e < a.d_v) *reinterpret_cast<uint4*>(out + 2 * e) = make_uint4(w[e], w[e + 1], w[e + 2], w[e + 3]);
           }
         }
       }
@@ -435,40 +444,18 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_mma_kernel(const __grid_co
     }
     __syncwarp();
   } else if (warp == kLoadWarp) {
-    // ------------------------------------------------ units and loads
-    int64_t units = 0;
-    for (int b = lane; b < a.batch; b += 32) units += seq_units(a, b);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) units += __shfl_xor_sync(0xffffffffu, units, o);
-    const int64_t total = units * a.H;
+    // ------------------------------------------------ loads
     uint32_t part = 0, tail = 0, busy = 0;       // parts loaded, parts known to be free again, units with keys
     int free_blocks = a.ring, slot = 0;
-    int64_t next = blockIdx.x / 2;
     bool ok = true;
     for (uint32_t un = 0; ok; ++un) {
-      Unit u;
-      if (rank == 0) {
-        u = find_unit(a, next, total, lane);
-        if (u.h >= 0 && lane == 0) next = static_cast<int64_t>(gridDim.x / 2) + atomicAdd(a.next_unit, 1u);
-        next = __shfl_sync(0xffffffffu, next, 0);
-        if (un >= 2) ok = __all_sync(0xffffffffu, bounded_wait_cluster(&sm.unit_empty[un & 1], ((un >> 1) - 1) & 1u, wc));
-        if (!ok) break;
-        if (lane == 0) {
-          sm.unit[un & 1] = u;
-          mbar_arrive(&sm.unit_full[un & 1]);
-          const uint32_t to = cluster_addr(&sm.unit[un & 1], 1), bar = cluster_addr(&sm.unit_full[un & 1], 1);
-          st_async_v4(to, make_uint4(u.q0, u.nq, u.k0, u.nk), bar);
-          st_async_v4(to + 16, make_uint4(u.row0, u.h, 0u, 0u), bar);
-        }
-      } else {
-        if (lane == 0) mbar_arrive_expect_tx(&sm.unit_full[un & 1], sizeof(Unit));
-        ok = __all_sync(0xffffffffu, bounded_wait_cluster(&sm.unit_full[un & 1], (un >> 1) & 1u, wc));
-        if (!ok) break;
-        u = sm.unit[un & 1];
-      }
+      ok = __all_sync(0xffffffffu, bounded_wait_cluster(&sm.unit_full[un & 1], (un >> 1) & 1u, wc));
+      if (!ok) break;
+      const Unit u = sm.unit[un & 1];
       if (u.h < 0) break;
       const int n0 = key_tiles(a, u, 0), n1 = key_tiles(a, u, 1), nt = max(n0, n1);
-      if (rank == 1 && lane == 0) mbar_arrive_relaxed_at(cluster_addr(&sm.unit_empty[un & 1], 0));
+      __syncwarp();
+      if (lane == 0) mbar_arrive_relaxed_at(cluster_addr(&sm.unit_empty[un & 1], 0));
       if (nt == 0) continue;
       int good = 1;
       if (lane == 0) {
@@ -526,6 +513,38 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_mma_kernel(const __grid_co
         for (uint32_t f = part > kParts ? part - kParts : 0; f < part; ++f)
           drain_wait(&sm.full[f % kParts], (f / kParts) & 1u, kDrainNs);
         if (busy > 0) drain_wait(&sm.q_full, (busy - 1) & 1u, kDrainNs);
+      }
+    }
+    __syncwarp();
+  } else if (warp == kUnitWarp) {
+    // ------------------------------------------------ units, found ahead by the even CTA for both
+    if (rank == 0) {
+      int64_t units = 0;
+      for (int b = lane; b < a.batch; b += 32) units += seq_units(a, b);
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) units += __shfl_xor_sync(0xffffffffu, units, o);
+      const int64_t total = units * a.H;
+      int64_t next = blockIdx.x / 2;
+      for (uint32_t un = 0;; ++un) {
+        const Unit u = find_unit(a, next, total, lane);
+        if (u.h >= 0 && lane == 0) next = static_cast<int64_t>(gridDim.x / 2) + atomicAdd(a.next_unit, 1u);
+        next = __shfl_sync(0xffffffffu, next, 0);
+        if (un >= 2 && !__all_sync(0xffffffffu, bounded_wait_cluster(&sm.unit_empty[un & 1], ((un >> 1) - 1) & 1u, wc))) break;
+        if (lane == 0) {
+          sm.unit[un & 1] = u;
+          mbar_arrive(&sm.unit_full[un & 1]);
+          const uint32_t to = cluster_addr(&sm.unit[un & 1], 1), bar = cluster_addr(&sm.unit_full[un & 1], 1);
+          st_async_v4(to, make_uint4(u.q0, u.nq, u.k0, u.nk), bar);
+          st_async_v4(to + 16, make_uint4(u.row0, u.h, 0u, 0u), bar);
+        }
+        if (u.h < 0) break;
+      }
+    } else {
+      // the odd CTA expects them
+      for (uint32_t un = 0;; ++un) {
+        if (lane == 0) mbar_arrive_expect_tx(&sm.unit_full[un & 1], sizeof(Unit));
+        if (!__all_sync(0xffffffffu, bounded_wait_cluster(&sm.unit_full[un & 1], (un >> 1) & 1u, wc))) break;
+        if (sm.unit[un & 1].h < 0) break;
       }
     }
     __syncwarp();
