@@ -131,7 +131,7 @@ li_status norm_rope(li_ctx* c, const li_head_rows* sets, int n_sets, li_dtype dt
   if (grid >= (int64_t(1) << 31)) return fail(c, LI_ERR_SHAPE, "%s: too many tokens (%lld)", what, static_cast<long long>(n_tok));
   if ((s = check_device(c, what)) != LI_OK) return s;
   (void)cudaGetLastError();
-  Launch L(c, st, "norm_rope", static_cast<int>(grid), plan.lanes ? 256 : 128, 0);
+  Launch L(c, st, "norm_rope", static_cast<int>(grid), 32 * plan.warps, 0);
   const cudaError_t e = launch_norm_rope(a, dtype, plan, grid, st);
   L.done();
   return e == cudaSuccess ? LI_OK : cuda_fail(c, e, "norm_rope launch");
@@ -335,18 +335,22 @@ li_status prompt_mma(li_ctx* c, const li_prompt& p, void* out, float* lse, void*
   a.d_nope = p.d_nope;
   a.d_rope = p.d_rope;
   a.d_v = p.d_v;
-  if (!prompt_mma_layout(&a, c->num_sms, c->max_smem_optin))
+  // Pairs of CTAs halve what an SM reads of keys and values, but their units are twice as many queries and take longer
+  // to begin and end.  Measured at d 192/128 (single CTAs, pairs): 8 sequences of up to 257 x 16 heads 20, 30 us; 4 of
+  // 2048 x 32 202, 219; 1 of 4096 x 32 220, 202; 4 of up to 4096 x 16 221, 197; 1 of 8192 x 32 723, 656.
+  const bool pair = p.max_q > 2048;
+  if (!(pair ? prompt_pair_layout(&a, c->num_sms, c->max_smem_optin) : prompt_mma_layout(&a, c->num_sms, c->max_smem_optin)))
     return fail(c, LI_ERR_UNSUPPORTED, "%s: operands too large for shared memory", what);
   li_status s = rows_map(c, &a.map_q, p.q, 128, p.d_nope + p.d_rope, p.H, p.total_q, p.q_head_stride, p.q_tok_stride);
   if (s == LI_OK && p.total_k > 0) {
-    s = rows_map(c, &a.map_k, p.k_nope, 64, p.d_nope, p.H, p.total_k, p.k_head_stride, p.k_tok_stride);
-    if (s == LI_OK) s = rows_map(c, &a.map_v, p.v, 64, p.d_v, p.H, p.total_k, p.v_head_stride, p.v_tok_stride);
-    if (s == LI_OK && p.d_rope) s = rows_map(c, &a.map_kr, p.k_rope, 64, p.d_rope, 0, p.total_k, 0, p.kr_tok_stride);
+    s = rows_map(c, &a.map_k, p.k_nope, a.box_rows, p.d_nope, p.H, p.total_k, p.k_head_stride, p.k_tok_stride);
+    if (s == LI_OK) s = rows_map(c, &a.map_v, p.v, a.box_rows, p.d_v, p.H, p.total_k, p.v_head_stride, p.v_tok_stride);
+    if (s == LI_OK && p.d_rope) s = rows_map(c, &a.map_kr, p.k_rope, a.box_rows, p.d_rope, 0, p.total_k, 0, p.kr_tok_stride);
   }
   if (s != LI_OK) return s;
   (void)cudaGetLastError();
-  Launch L(c, st, "prompt_attn", a.grid, 640, static_cast<int>(a.smem_bytes));
-  const cudaError_t e = launch_prompt_mma(a, st);
+  Launch L(c, st, pair ? "prompt_pair" : "prompt_attn", a.grid, pair ? 640 : 352, static_cast<int>(a.smem_bytes));
+  const cudaError_t e = pair ? launch_prompt_pair(a, st) : launch_prompt_mma(a, st);
   L.done();
   return e == cudaSuccess ? LI_OK : cuda_fail(c, e, "prompt attention launch");
 }

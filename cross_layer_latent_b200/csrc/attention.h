@@ -108,9 +108,9 @@ cudaError_t launch_latent_join(const LatentMmaArgs& a, cudaStream_t st);
 
 struct alignas(64) PromptMmaArgs {
   CUtensorMap map_q;      // dims {d_nope + d_rope, H, total_q}, box {64, 1, 128}
-  CUtensorMap map_k;      // dims {d_nope, H, total_k}, box {64, 1, 64}
-  CUtensorMap map_kr;     // dims {d_rope, total_k}, box {64, 64}
-  CUtensorMap map_v;      // dims {d_v, H, total_k}, box {64, 1, 64}
+  CUtensorMap map_k;      // dims {d_nope, H, total_k}, box {64, 1, box_rows}
+  CUtensorMap map_kr;     // dims {d_rope, total_k}, box {64, box_rows}
+  CUtensorMap map_v;      // dims {d_v, H, total_k}, box {64, 1, box_rows}
   const int32_t* cu_q;
   const int32_t* cu_k;
   void* out;
@@ -125,16 +125,19 @@ struct alignas(64) PromptMmaArgs {
   int wide_out;           // every output row is 32-byte aligned
   int batch, H, total_q, total_k, max_q;
   int d_nope, d_rope, d_v;
-  // filled by prompt_mma_layout
-  int nope_blocks, rope_blocks;             // 64-column blocks
+  // filled by prompt_mma_layout or prompt_pair_layout
+  int box_rows;                             // rows of a block of keys or values
+  int nope_blocks, rope_blocks, v_blocks;   // 64-column blocks
   int nope_ksteps, rope_ksteps;             // 16-element K steps of each part's last block
-  int ring;                                 // 8 KB blocks of the ring
+  int ring;                                 // blocks of the ring
   int grid;
   uint32_t smem_bytes;
 };
 
-bool prompt_mma_layout(PromptMmaArgs* a, int num_sms, int max_smem);
+bool prompt_mma_layout(PromptMmaArgs* a, int num_sms, int max_smem);     // one CTA a unit (prompt_mma.cu)
 cudaError_t launch_prompt_mma(const PromptMmaArgs& a, cudaStream_t st);
+bool prompt_pair_layout(PromptMmaArgs* a, int num_sms, int max_smem);    // two (prompt_pair.cu)
+cudaError_t launch_prompt_pair(const PromptMmaArgs& a, cudaStream_t st);
 
 // fp32 (attn_rows.cu).
 cudaError_t launch_latent_attn_rows(const LatentAttnArgs& a, cudaStream_t st);

@@ -293,6 +293,12 @@ __device__ __forceinline__ float2 exp2_poly(uint64_t x) {
                      __int_as_float(__float_as_int(m.y) + (__float_as_int(e.y) << 23)));
 }
 
+// At least `ns` nanoseconds on an SM.
+__device__ __forceinline__ void delay_ns(uint64_t ns) {
+  const uint64_t t0 = cycles();
+  while (cycles() - t0 < ns * kCyclesPerNs) __nanosleep(1000);
+}
+
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   uint32_t r;
   asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));

@@ -1,176 +1,89 @@
 // prompt_mma.cu -- latent attention in expanded form on the tensor cores:
 // causal (or full) attention of ragged prompts, head by head.
 //
-// Two CTAs on neighbouring SMs work as a pair (cta_group::2 MMAs of M = 256).
-// A unit of work is 512 queries of one head, as two tiles of 256, half of the
-// rows of each in either CTA, and a walk over the keys in tiles of 128:
-//     S_q = Q_q K^T      [256 x 128]   A = Q, B = K (both K-major in shared memory)
-//     P_q = exp2(S_q - m)              one query row to two threads
-//     O_q += P_q V       [256 x 128]   A = P from tensor memory, B = V (MN-major)
+// A unit of work is 256 queries of one head, as two tiles of 128, and a walk
+// over the keys in tiles of 128:
+//     S_q = Q_q K^T      [128 x 128]   A = Q, B = K (both K-major in shared memory)
+//     P_q = exp2(S_q - m)              one query row a thread
+//     O_q += P_q V       [128 x d_v]   A = P from tensor memory, B = V (MN-major)
 // The two tiles alternate: while one's scores are turned into weights, the
-// other's products run.  At d_nope + d_rope = 192, d_v = 128 two tiles cost
-// 2560 cycles of MMA (12 steps of 64 and 8 of 64 for each).
-// The pair halves what an SM holds and reads of the keys and values: 64 keys
-// of K and 64 columns of V, 40 KB a key tile instead of 80.  Single CTAs with
-// 256 queries had room for 1.6 key tiles next to their queries, and their
-// loads, issued 1300 cycles ahead, came 800 too late (4,100 cycles for the two
-// tiles without any softmax, 732 us for 8192 tokens of 32 heads).
+// other's products run, so the tensor cores wait for neither.  At d_nope +
+// d_rope = 192, d_v = 128 a tile pair costs 2560 cycles of MMA (12 steps of 64
+// and 8 of 64 for each tile) against 2048 cycles of special-function unit (128
+// x 128 exponentials a tile at 16 a cycle): the MMAs bound it.
 // Tensor memory is full: S0, S1 (P takes the place of S), O0, O1.  Shared
-// memory holds the CTA's rows of both query tiles (96 KB) and a ring of 8 KB
-// blocks of 64 rows x 64 columns.  A key tile has two parts in the ring, its K
-// blocks (k_nope of the head, then the k_rope that all heads share) and its V
-// blocks, each with one barrier in the even CTA, which issues the MMAs.
+// memory holds both query tiles (96 KB) and a ring of 16 KB blocks, 128
+// tokens x 64 columns of K (k_nope of the head, then the k_rope that all heads
+// share) or of V.  A key tile has two parts in the ring, its K blocks and its
+// V blocks, each with one barrier: eight blocks hold 1.6 tiles, and a part is
+// loaded at least 1280 cycles of MMA before it is needed.
 //
 // The running maximum moves only when a row exceeds it by more than 8 (in
 // powers of two): weights stay below 256, which costs their bf16 rounding
 // (relative) and the fp32 sums nothing, and the outputs are seldom rescaled.
 // The sums are taken before the weights are rounded.
 //
-// The pairs are persistent; units of a group of heads whose keys and values
-// fit the L2 together come longest first, from a counter that the even CTA
-// draws on for both (dealt out in turn, the slowest pair had 20% more work).
+// CTAs are persistent and take the next unit (prompt_units.cuh) from a counter.
+// prompt_pair.cu does the same work by pairs of CTAs, better for long
+// sequences: there the loads of this kernel, of whole key tiles for one SM,
+// come too late.
 #include <algorithm>
 
 #include "attention.h"
 #include "attn_sm100.cuh"
 #include "internal.h"
+#include "prompt_units.cuh"
 
 namespace li {
 
 namespace {
 
-constexpr int kTile = 128;
-constexpr int kPairRows = 2 * kTile;             // queries of a tile of the pair
-constexpr int kRows = 2 * kPairRows;             // and of a unit
-constexpr int kQBlockBytes = kTile * 128;        // 128 rows x 64 bf16
-constexpr int kBlockBytes = 64 * 128;            // 64 rows x 64 bf16
-constexpr int kVBlocks = 2;                      // blocks of a V part: 128 keys x 64 columns
-constexpr int kSoftWarps = 16;                   // two warpgroups for each query tile, half of the keys each
-constexpr int kMmaWarp = 16, kLoadWarp = 17, kUnitWarp = 18;   // and one that zeroes
-constexpr int kThreads = 32 * 20;
-constexpr int kMaxRing = 24;
+using namespace prompt;
+
+constexpr int kRows = 2 * kTile;                 // queries of a unit
+constexpr int kBlockBytes = kTile * 128;
+constexpr int kSoftWarps = 8;                    // a warpgroup for each query tile
+constexpr int kMmaWarp = 8, kLoadWarp = 9;      // and one that zeroes
+constexpr int kThreads = 32 * 11;
+constexpr int kMaxRing = 13;
 constexpr int kParts = 8;                        // parts in flight at most (a power of two)
-constexpr int kPolyOf = 4;                       // of so many pairs of exponentials one is computed on the FMA pipes
 constexpr float kGrow = 8.f;
 constexpr float kNoMax = -1e30f;
 constexpr uint64_t kDrainNs = 1000ull * 1000ull;
-constexpr int64_t kL2Share = int64_t(48) << 20;  // keys and values of the heads that run together
-
-struct alignas(16) Unit {
-  int q0, nq, k0, nk;    // rows of the sequence in q and k
-  int row0, h;           // first query of the unit; h < 0: no more units
-  int pad[2];
-};
 
 struct Smem {
-  uint64_t full[kParts], empty[kParts], raw[kParts];   // full, q_full, p_full, o_empty, unit_empty: the even CTA's count
+  uint64_t full[kParts], empty[kParts], raw[kParts];
   uint64_t unit_full[2], unit_empty[2];
   uint64_t q_full, q_empty, s_full[2], p_full[2], o_full[2], o_empty[2], drain;
   Unit unit[2];
-  float part[2][2][kTile];                       // by query tile, half of the keys and row
   uint32_t tmem;
   int abort_flag;
 };
-
-// Keys that query i of the sequence sees.
-__device__ __forceinline__ int key_limit(const PromptMmaArgs& a, const Unit& u, int i) {
-  if (!a.causal) return u.nk;
-  const int64_t n = static_cast<int64_t>(i) + 1 + u.nk - u.nq;
-  return static_cast<int>(max(min(n, static_cast<int64_t>(u.nk)), int64_t(0)));
-}
-// Key tiles of the pair's query tile q (0 or 1) of the unit: those that its last row sees.
-__device__ __forceinline__ int key_tiles(const PromptMmaArgs& a, const Unit& u, int q) {
-  const int first = u.row0 + q * kPairRows;
-  if (first >= u.nq) return 0;
-  return (key_limit(a, u, min(first + kPairRows, u.nq) - 1) + kTile - 1) / kTile;
-}
-
-__device__ __forceinline__ int seq_rows(const int32_t* cu, int b, int total, int* first) {
-  const int x = min(max(cu[b], 0), total);
-  *first = x;
-  return min(max(cu[b + 1], x), total) - x;
-}
-__device__ __forceinline__ int seq_queries(const PromptMmaArgs& a, int b, int* first) {
-  return min(seq_rows(a.cu_q, b, a.total_q, first), a.max_q);
-}
-__device__ __forceinline__ int seq_units(const PromptMmaArgs& a, int b) {
-  int f;
-  return (seq_queries(a, b, &f) + kRows - 1) / kRows;
-}
-
-// Unit number x of all (the whole warp calls it).
-__device__ __forceinline__ Unit find_unit(const PromptMmaArgs& a, int64_t x, int64_t total, int lane) {
-  Unit u;
-  u.h = -1;
-  if (x >= total) return u;
-  int b = a.batch - 1;
-  for (int b0 = 0; b0 < a.batch; b0 += 32) {
-    const int64_t c = b0 + lane < a.batch ? static_cast<int64_t>(seq_units(a, b0 + lane)) * a.H : 0;
-    int64_t end = c;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int64_t v = __shfl_up_sync(0xffffffffu, end, o);
-      if (lane >= o) end += v;
-    }
-    const int past = __popc(__ballot_sync(0xffffffffu, b0 + lane < a.batch && end <= x));
-    if (past < min(32, a.batch - b0)) {
-      b = b0 + past;
-      x -= __shfl_sync(0xffffffffu, end - c, past);
-      break;
-    }
-    x -= __shfl_sync(0xffffffffu, end, 31);
-  }
-  int f;
-  u.nq = seq_queries(a, b, &u.q0);
-  (void)f;
-  u.nk = seq_rows(a.cu_k, b, a.total_k, &u.k0);
-  // causal limits go by the whole sequence, also where max_q cuts it
-  int whole = seq_rows(a.cu_q, b, a.total_q, &f);
-  if (a.causal && whole > u.nq) u.nk = max(u.nk - (whole - u.nq), 0);
-  const int tiles = (u.nq + kRows - 1) / kRows;
-  const int64_t per_head = static_cast<int64_t>(max(u.nk, 1)) * (a.d_nope + a.d_v) * 2;
-  const int hg = static_cast<int>(max(min(kL2Share / per_head, static_cast<int64_t>(a.H)), int64_t(1)));
-  const int64_t per_group = static_cast<int64_t>(hg) * tiles;
-  const int g = static_cast<int>(x / per_group);
-  const int r = static_cast<int>(x - g * per_group);
-  const int heads = min(hg, a.H - g * hg);
-  u.h = g * hg + r % heads;
-  u.row0 = (tiles - 1 - r / heads) * kRows;
-  return u;
-}
-
-// 32 bytes in one store (p 32-byte aligned).
-__device__ __forceinline__ void st_global_32(void* p, const uint32_t* w) {
-  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]),
-               "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
-               : "memory");
-}
 
 __global__ void __launch_bounds__(kThreads, 1) prompt_mma_kernel(const __grid_constant__ PromptMmaArgs a) {
   extern __shared__ uint8_t raw_smem[];
   uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw_smem) + 1023) & ~uintptr_t(1023));
   const int nkb = a.nope_blocks + a.rope_blocks;
-  uint8_t* ring = base + 2 * nkb * kQBlockBytes;
+  uint8_t* ring = base + 2 * nkb * kBlockBytes;
   Smem& sm = *reinterpret_cast<Smem*>(ring + a.ring * kBlockBytes);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int rank = static_cast<int>(cluster_rank());
   const WaitCtl wc{&sm.abort_flag, a.status, a.wait_ns};
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < kParts; ++i) {
-      mbar_init(&sm.full[i], 2);
+      mbar_init(&sm.full[i], 1);
       mbar_init(&sm.empty[i], 1);
       mbar_init(&sm.raw[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sm.unit_full[i], 1);
-      mbar_init(&sm.unit_empty[i], 2 * kSoftWarps + 5);   // MMA issue, and softmax, loads and zeroes of both CTAs
+      mbar_init(&sm.unit_empty[i], kSoftWarps + 2);
       mbar_init(&sm.s_full[i], 1);
-      mbar_init(&sm.p_full[i], 16);
+      mbar_init(&sm.p_full[i], 4);
       mbar_init(&sm.o_full[i], 1);
-      mbar_init(&sm.o_empty[i], 16);
+      mbar_init(&sm.o_empty[i], 4);
     }
-    mbar_init(&sm.q_full, 2);
+    mbar_init(&sm.q_full, 1);
     mbar_init(&sm.q_empty, 1);
     mbar_init(&sm.drain, 1);
     sm.abort_flag = 0;
@@ -182,142 +95,115 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_mma_kernel(const __grid_co
     }
   }
   if (warp == kMmaWarp) {
-    tmem2_alloc(&sm.tmem, 512);
+    tmem_alloc(&sm.tmem, 512);
+    tmem_relinquish();
   }
   pdl_begin();
   tc_fence_before();
-  cluster_sync();                                // the barriers of both CTAs are there
+  __syncthreads();
   tc_fence_after();
   const uint32_t tmem = sm.tmem;
 
   if (warp < kSoftWarps) {
     // ------------------------------------------------ softmax and output of query tile q
-    // A row has two threads, one for 64 of a tile's keys: with 128 keys a thread, a warp alone on its scheduler
-    // took 2100 cycles a tile, most of them waiting for its own results.
-    const int q = warp >> 3, half = (warp >> 2) & 1, quad = warp & 3;
+    const int q = warp >> 2, quad = warp & 3;
     const uint32_t lanes = static_cast<uint32_t>(quad * 32) << 16;
     const uint32_t s_tm = tmem + q * 128 + lanes, o_tm = tmem + 256 + q * 128 + lanes;
     const int r = quad * 32 + lane;
-    const int bar = 1 + q * 4 + quad;            // the two warps of these 32 rows
-    const uint32_t u_bar[2] = {cluster_addr(&sm.unit_empty[0], 0), cluster_addr(&sm.unit_empty[1], 0)};
-    constexpr int my_cols = 64;                  // output columns of a half
-    const uint32_t p_bar = cluster_addr(&sm.p_full[q], 0), o_bar = cluster_addr(&sm.o_empty[q], 0);
     uint32_t tile = 0, outs = 0;
     bool ok = true;
     for (uint32_t un = 0; ok; ++un) {
-      ok = bounded_wait_cluster(&sm.unit_full[un & 1], (un >> 1) & 1u, wc);
-      ok = !named_bar_any(bar, 64, !ok);
+      ok = __all_sync(0xffffffffu, bounded_wait_sleep(&sm.unit_full[un & 1], (un >> 1) & 1u, wc));
       if (!ok) break;
       const Unit u = sm.unit[un & 1];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm.unit_empty[un & 1]);
       if (u.h < 0) break;
-      const int n = key_tiles(a, u, q);
-      const int i = u.row0 + q * kPairRows + rank * kTile + r;
+      const int first = u.row0 + q * kTile;
+      const int n = key_tiles<kRows>(a, u, q);
+      const int i = first + r;
       const int lim = i < u.nq ? key_limit(a, u, i) : u.nk;
       float m = kNoMax, l = 0.f;
       for (int t = 0; t < n; ++t, ++tile) {
-        ok = bounded_wait(&sm.s_full[q], tile & 1u, wc);
-        __syncwarp();
+        ok = __all_sync(0xffffffffu, bounded_wait(&sm.s_full[q], tile & 1u, wc));
+        if (!ok) break;
         tc_fence_after();
-        float x[64];
+        float x[128];
         {
-          uint32_t xr[2][32];
-          tmem_ld<32>(s_tm + 64 * half, xr[0]);
-          tmem_ld<32>(s_tm + 64 * half + 32, xr[1]);
+          uint32_t xr[4][32];
+#pragma unroll
+          for (int c = 0; c < 4; ++c) tmem_ld<32>(s_tm + 32 * c, xr[c]);
           tmem_wait_ld();
 #pragma unroll
-          for (int c = 0; c < 64; ++c) x[c] = __uint_as_float(xr[c / 32][c % 32]);
+          for (int c = 0; c < 128; ++c) x[c] = __uint_as_float(xr[c / 32][c % 32]);
         }
         if (a.negate) {
 #pragma unroll
-          for (int c = 0; c < 64; ++c) x[c] = -x[c];
+          for (int c = 0; c < 128; ++c) x[c] = -x[c];
         }
-        const int left = lim - t * kTile - 64 * half;
-        if (__any_sync(0xffffffffu, left < 64)) {
+        if (__any_sync(0xffffffffu, (t + 1) * kTile > lim)) {
+          const int left = lim - t * kTile;
 #pragma unroll
-          for (int c = 0; c < 64; ++c)
+          for (int c = 0; c < 128; ++c)
             if (c >= left) x[c] = -INFINITY;
         }
         float top4[4] = {x[0], x[1], x[2], x[3]};
 #pragma unroll
-        for (int c = 4; c < 60; c += 8)
+        for (int c = 4; c < 124; c += 8)
 #pragma unroll
           for (int e = 0; e < 4; ++e) top4[e] = fmaxf(fmaxf(top4[e], x[c + e]), x[c + 4 + e]);
-        float top = fmaxf(fmaxf(fmaxf(top4[0], x[60]), fmaxf(top4[1], x[61])), fmaxf(fmaxf(top4[2], x[62]), fmaxf(top4[3], x[63])));
-        // every score of the tile has been read when this returns
-        if (named_bar_any(bar, 64, (top - m) * a.scale_log2 > kGrow || !ok)) {
-          sm.part[q][half][r] = top;
-          if (named_bar_any(bar, 64, !ok)) {
-            ok = false;
-            break;
-          }
-          top = fmaxf(top, sm.part[q][half ^ 1][r]);
-          const bool grow = (top - m) * a.scale_log2 > kGrow;
-          if (__any_sync(0xffffffffu, grow)) {
-            const float now = grow ? top : m;
-            const float keep = exp2_fast((m - now) * a.scale_log2);
-            m = now;
-            l *= keep;
-            if (t > 0) {
-              // the previous tile's product is complete: s_full was committed after it
+        const float top = fmaxf(fmaxf(fmaxf(top4[0], x[124]), fmaxf(top4[1], x[125])), fmaxf(fmaxf(top4[2], x[126]), fmaxf(top4[3], x[127])));
+        const bool grow = (top - m) * a.scale_log2 > kGrow;
+        if (__any_sync(0xffffffffu, grow)) {
+          const float now = grow ? top : m;
+          const float keep = exp2_fast((m - now) * a.scale_log2);
+          m = now;
+          l *= keep;
+          if (t > 0) {
+            // the previous tile's product is complete: s_full was committed after it
 #pragma unroll 1
-              for (int c = half * my_cols; c < (half + 1) * my_cols; c += 16) {
-                uint32_t o[16];
-                tmem_ld<16>(o_tm + c, o);
-                tmem_wait_ld();
+            for (int c = 0; c < a.v_blocks * 64; c += 16) {
+              uint32_t o[16];
+              tmem_ld<16>(o_tm + c, o);
+              tmem_wait_ld();
 #pragma unroll
-                for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * keep);
-                tmem_st<16>(o_tm + c, o);
-              }
+              for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * keep);
+              tmem_st<16>(o_tm + c, o);
             }
           }
         }
         const float ms = m * a.scale_log2;
-        const uint64_t sc = pair(a.scale_log2, a.scale_log2), off = pair(-ms, -ms);
-        uint64_t s0 = 0, s1 = 0;                 // pairs of zeros
+        float s0 = 0.f, s1 = 0.f;
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
+        for (int c = 0; c < 128; c += 32) {
           uint32_t pk[16];
 #pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            const uint64_t y = fma2(pair(x[32 * c + 2 * e], x[32 * c + 2 * e + 1]), sc, off);
-            float2 p;
-            if (e % kPolyOf == kPolyOf - 1) {
-              p = exp2_poly(y);
-            } else {
-              const float2 v = unpair(y);
-              p = make_float2(exp2_fast(v.x), exp2_fast(v.y));
-            }
-            if (e & 1) s1 = add2(s1, pair(p.x, p.y));
-            else s0 = add2(s0, pair(p.x, p.y));
-            pk[e] = pack_bf16(p.x, p.y);
+          for (int e = 0; e < 32; e += 2) {
+            const float p0 = exp2_fast(fmaf(x[c + e], a.scale_log2, -ms));
+            const float p1 = exp2_fast(fmaf(x[c + e + 1], a.scale_log2, -ms));
+            s0 += p0;
+            s1 += p1;
+            pk[e / 2] = pack_bf16(p0, p1);
           }
-          tmem_st<16>(s_tm + 32 * half + 16 * c, pk);
+          tmem_st<16>(s_tm + c / 2, pk);
         }
+        l += s0 + s1;
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive_relaxed_at(p_bar);
-        const float2 sum = unpair(add2(s0, s1));
-        l += sum.x + sum.y;
+        if (lane == 0) mbar_arrive(&sm.p_full[q]);
       }
       if (!ok) break;
-      __syncwarp();
-      if (lane == 0) mbar_arrive_relaxed_at(u_bar[un & 1]);   // the unit's numbers have been used
-      if (u.row0 + q * kPairRows >= u.nq) continue;
-      // the row's sum: both halves, after the last tile's maxima have been read
-      if (lim <= 0) l = 0.f;                     // nothing to attend
-      named_bar_sync(bar, 64);
-      sm.part[q][half][r] = l;
-      ok = n == 0 || bounded_wait(&sm.o_full[q], outs & 1u, wc);
-      if (named_bar_any(bar, 64, !ok)) {
-        ok = false;
-        break;
+      if (first >= u.nq) continue;
+      if (n > 0) {
+        ok = __all_sync(0xffffffffu, bounded_wait(&sm.o_full[q], outs & 1u, wc));
+        if (!ok) break;
+        ++outs;
+        tc_fence_after();
       }
-      l += sm.part[q][half ^ 1][r];
-      tc_fence_after();
       const float inv = l > 0.f ? 1.f / l : 0.f;
       const int64_t row = static_cast<int64_t>(u.q0 + i) * a.H + u.h;
-      for (int c = half * my_cols; c < min((half + 1) * my_cols, a.d_v); c += 32) {
+      for (int c = 0; c < a.d_v; c += 32) {
         uint32_t o[32];
         if (n > 0) {
           tmem_ld<32>(o_tm + c, o);
@@ -327,38 +213,27 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_mma_kernel(const __grid_co
           for (int e = 0; e < 32; ++e) o[e] = 0u;
         }
         if (i < u.nq) {
-          __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out) + row * a.d_v + c;
           uint32_t w[16];
 #pragma unroll
           for (int e = 0; e < 16; ++e) w[e] = pack_bf16(__uint_as_float(o[2 * e]) * inv, __uint_as_float(o[2 * e + 1]) * inv);
-          // rows lie apart, so a store takes as many cycles as it has rows: 32 bytes a thread where they are aligned
-          if (a.wide_out) {
-#pragma unroll
-            for (int e = 0; e < 16; e += 8)
-              if (c + 2 * e < a.d_v) st_global_32(out + 2 * e, &w[e]);
-          } else {
-#pragma unroll
-            for (int e = 0; e < 16; e += 4)
-              if (c + 2 * e < a.d_v) *reinterpret_cast<uint4*>(out + 2 * e) = make_uint4(w[e], w[e + 1], w[e + 2], w[e + 3]);
-          }
+          store_row32(static_cast<__nv_bfloat16*>(a.out) + row * a.d_v + c, w, a.d_v - c, a.wide_out);
         }
       }
-      if (a.lse && half == 0 && i < u.nq) a.lse[row] = l > 0.f ? (m * a.scale_log2 + log2f(l)) * 0.69314718056f : -INFINITY;
+      if (a.lse && i < u.nq) a.lse[row] = l > 0.f ? (m * a.scale_log2 + log2f(l)) * 0.69314718056f : -INFINITY;
       if (n > 0) {
-        ++outs;
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive_relaxed_at(o_bar);
+        if (lane == 0) mbar_arrive(&sm.o_empty[q]);
       }
     }
   } else if (warp == kMmaWarp) {
-    // ------------------------------------------------ MMA issue, one lane of the even CTA
-    if (rank == 0 && elect_one()) {
-      const uint32_t id_s = make_instr_desc(1, 256, 128);
-      const uint32_t id_o = id_s | kMajorMnB;
+    // ------------------------------------------------ MMA issue, one lane
+    if (elect_one()) {
+      const uint32_t id_s = make_instr_desc(1, 128, 128);
+      const uint32_t id_o = make_instr_desc(1, 128, 64) | kMajorMnB;
       const uint32_t q0 = desc_lo(smem_addr(base), 0), r0 = desc_lo(smem_addr(ring), 0);
-      constexpr uint32_t kBlockStep = kBlockBytes >> 4, kQStep = kQBlockBytes >> 4;
-      const int per = nkb + kVBlocks;
+      constexpr uint32_t kBlockStep = kBlockBytes >> 4;
+      const int per = nkb + a.v_blocks;
       int kc = 0, vc = nkb;                      // ring positions of the next K part and V part
       uint32_t kp = 0, vp = 1;                   // and their numbers
       auto advance = [&](int& c, uint32_t& p) {
@@ -373,89 +248,97 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_mma_kernel(const __grid_co
       for (uint32_t un = 0; ok; ++un) {
         if (!(ok = bounded_wait(&sm.unit_full[un & 1], (un >> 1) & 1u, wc))) break;
         const Unit u = sm.unit[un & 1];
-        if (u.h < 0) break;
-        const int n0 = key_tiles(a, u, 0), n1 = key_tiles(a, u, 1), nt = max(n0, n1);
         mbar_arrive(&sm.unit_empty[un & 1]);
+        if (u.h < 0) break;
+        const int n0 = key_tiles<kRows>(a, u, 0), n1 = key_tiles<kRows>(a, u, 1), nt = max(n0, n1);
         if (nt == 0) continue;
-        if (!(ok = bounded_wait_cluster(&sm.q_full, busy & 1u, wc))) break;
+        if (!(ok = bounded_wait(&sm.q_full, busy & 1u, wc))) break;
         ++busy;
         bool k_here = false, v_here = false;
         // S_q of the next K part; `last`: no other tile needs the part
         auto scores = [&](int q, bool last) {
-          if (!k_here && !bounded_wait_cluster(&sm.full[kp % kParts], (kp / kParts) & 1u, wc)) return false;
+          if (!k_here && !bounded_wait(&sm.full[kp % kParts], (kp / kParts) & 1u, wc)) return false;
           k_here = true;
           tc_fence_after();
-          uint32_t da = q0 + q * nkb * kQStep;
+          uint32_t da = q0 + q * nkb * kBlockStep;
           int s = kc;
-          for (int j = 0; j < nkb; ++j, da += kQStep) {
+          for (int j = 0; j < nkb; ++j, da += kBlockStep) {
             const uint32_t db = r0 + s * kBlockStep;
             if (++s == a.ring) s = 0;
             const int ks = j == a.nope_blocks - 1 ? a.nope_ksteps : (j == nkb - 1 ? a.rope_ksteps : 4);
             if (ks == 4) {
-              umma2_ss_steps<4, 2, 2>(tmem + q * 128, da, db, id_s, j > 0 ? 1u : 0u);
+              umma_ss_steps<4, 2, 2>(tmem + q * 128, da, db, id_s, j > 0 ? 1u : 0u);
             } else {
-              for (int k = 0; k < ks; ++k) umma2_ss_steps<1, 2, 2>(tmem + q * 128, da + 2 * k, db + 2 * k, id_s, j + k > 0 ? 1u : 0u);
+              for (int k = 0; k < ks; ++k) umma_ss_steps<1, 2, 2>(tmem + q * 128, da + 2 * k, db + 2 * k, id_s, j + k > 0 ? 1u : 0u);
             }
           }
           if (last) {
-            umma2_commit(&sm.empty[kp % kParts]);
+            umma_commit(&sm.empty[kp % kParts]);
             advance(kc, kp);
             k_here = false;
           }
-          umma2_commit(&sm.s_full[q]);
+          umma_commit(&sm.s_full[q]);
           return true;
         };
         // O_q of the next V part
         auto values = [&](int q, bool first, bool final, bool last) {
-          if (first && outs[q] > 0 && !bounded_wait_cluster(&sm.o_empty[q], (outs[q] - 1) & 1u, wc)) return false;
-          if (!v_here && !bounded_wait_cluster(&sm.full[vp % kParts], (vp / kParts) & 1u, wc)) return false;
+          if (first && outs[q] > 0 && !bounded_wait(&sm.o_empty[q], (outs[q] - 1) & 1u, wc)) return false;
+          if (!v_here && !bounded_wait(&sm.full[vp % kParts], (vp / kParts) & 1u, wc)) return false;
           v_here = true;
-          if (!bounded_wait_cluster(&sm.p_full[q], ptile[q] & 1u, wc)) return false;
+          if (!bounded_wait(&sm.p_full[q], ptile[q] & 1u, wc)) return false;
           ++ptile[q];
           tc_fence_after();
           int s = vc;
-          for (int j = 0; j < kVBlocks; ++j) {   // 64 keys each
-            umma2_ts_steps<4, 128>(tmem + 256 + q * 128, tmem + q * 128 + j * 32, r0 + s * kBlockStep, id_o, first && j == 0 ? 0u : 1u);
+          for (int j = 0; j < a.v_blocks; ++j) {
+            umma_ts_steps<8, 128>(tmem + 256 + q * 128 + j * 64, tmem + q * 128, r0 + s * kBlockStep, id_o, first ? 0u : 1u);
             if (++s == a.ring) s = 0;
           }
           if (last) {
-            umma2_commit(&sm.empty[vp % kParts]);
+            umma_commit(&sm.empty[vp % kParts]);
             advance(vc, vp);
             v_here = false;
           }
           if (final) {
-            umma2_commit(&sm.o_full[q]);
+            umma_commit(&sm.o_full[q]);
             ++outs[q];
           }
           return true;
         };
-        for (int t = -1; t < nt && ok; ++t) {
-          for (int q = 0; q < 2 && ok; ++q) {
-            const int n = q == 0 ? n0 : n1;
-            if (t >= 0 && t < n) ok = values(q, t == 0, t == n - 1, q == 1 || t >= n1);
-            if (ok && t + 1 < n) ok = scores(q, q == 1 || t + 1 >= n1);
-          }
-          if (ok && t + 2 == nt) umma2_commit(&sm.q_empty);
+        if (n0 > 0) ok = scores(0, n1 == 0);
+        if (ok && n1 > 0) ok = scores(1, true);
+        if (ok && nt == 1) umma_commit(&sm.q_empty);
+        for (int t = 0; t < nt && ok; ++t) {
+          if (t < n0) ok = values(0, t == 0, t == n0 - 1, t >= n1);
+          if (ok && t + 1 < n0) ok = scores(0, t + 1 >= n1);
+          if (ok && t < n1) ok = values(1, t == 0, t == n1 - 1, true);
+          if (ok && t + 1 < n1) ok = scores(1, true);
+          if (ok && t + 2 == nt) umma_commit(&sm.q_empty);
         }
       }
       // nothing is in flight when the CTA ends, whichever role gave up
-      umma2_commit(&sm.drain);
+      umma_commit(&sm.drain);
       drain_wait(&sm.drain, 0, kDrainNs);
     }
     __syncwarp();
   } else if (warp == kLoadWarp) {
-    // ------------------------------------------------ loads
+    // ------------------------------------------------ units and loads
+    const int64_t total = all_units<kRows>(a, lane);
+    int64_t next = blockIdx.x;
     uint32_t part = 0, tail = 0, busy = 0;       // parts loaded, parts known to be free again, units with keys
     int free_blocks = a.ring, slot = 0;
     bool ok = true;
     for (uint32_t un = 0; ok; ++un) {
-      ok = __all_sync(0xffffffffu, bounded_wait_cluster(&sm.unit_full[un & 1], (un >> 1) & 1u, wc));
+      const Unit u = find_unit<kRows>(a, next, total, lane);
+      if (u.h >= 0 && lane == 0) next = static_cast<int64_t>(gridDim.x) + atomicAdd(a.next_unit, 1u);
+      next = __shfl_sync(0xffffffffu, next, 0);
+      if (un >= 2) ok = __all_sync(0xffffffffu, bounded_wait(&sm.unit_empty[un & 1], ((un >> 1) - 1) & 1u, wc));
       if (!ok) break;
-      const Unit u = sm.unit[un & 1];
+      if (lane == 0) {
+        sm.unit[un & 1] = u;
+        mbar_arrive(&sm.unit_full[un & 1]);
+      }
       if (u.h < 0) break;
-      const int n0 = key_tiles(a, u, 0), n1 = key_tiles(a, u, 1), nt = max(n0, n1);
-      __syncwarp();
-      if (lane == 0) mbar_arrive_relaxed_at(cluster_addr(&sm.unit_empty[un & 1], 0));
+      const int n0 = key_tiles<kRows>(a, u, 0), n1 = key_tiles<kRows>(a, u, 1), nt = max(n0, n1);
       if (nt == 0) continue;
       int good = 1;
       if (lane == 0) {
@@ -463,7 +346,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_mma_kernel(const __grid_co
         auto room = [&](int blocks) {
           while (free_blocks < blocks || part - tail >= kParts) {
             if (!bounded_wait(&sm.empty[tail % kParts], (tail / kParts) & 1u, wc)) return false;
-            free_blocks += tail & 1 ? kVBlocks : nkb;
+            free_blocks += tail & 1 ? a.v_blocks : nkb;
             ++tail;
           }
           free_blocks -= blocks;
@@ -477,29 +360,27 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_mma_kernel(const __grid_co
         if (busy > 0) good = bounded_wait(&sm.q_empty, (busy - 1) & 1u, wc);
         if (good) {
           const int tiles = n1 > 0 ? 2 : 1;
-          const uint32_t q_bar = cluster_addr(&sm.q_full, 0);
-          mbar_arrive_expect_tx_at(q_bar, tiles * nkb * kQBlockBytes);
+          mbar_arrive_expect_tx(&sm.q_full, tiles * nkb * kBlockBytes);
           ++busy;
           for (int q = 0; q < tiles; ++q)
             for (int j = 0; j < nkb; ++j)
-              tma2_load_3d(base + (q * nkb + j) * kQBlockBytes, &a.map_q, q_bar,
-                           j < a.nope_blocks ? 64 * j : a.d_nope + 64 * (j - a.nope_blocks), u.h,
-                           u.q0 + u.row0 + q * kPairRows + rank * kTile);
+              tma_load_3d(base + (q * nkb + j) * kBlockBytes, &a.map_q, &sm.q_full,
+                          j < a.nope_blocks ? 64 * j : a.d_nope + 64 * (j - a.nope_blocks), u.h, u.q0 + u.row0 + q * kTile);
           for (int t = 0; t < nt; ++t) {
             const int row = u.k0 + t * kTile;
             if (!(good = room(nkb))) break;
-            uint32_t bar = cluster_addr(&sm.full[part % kParts], 0);
-            mbar_arrive_expect_tx_at(bar, nkb * kBlockBytes);
+            uint64_t* bar = &sm.full[part % kParts];
+            mbar_arrive_expect_tx(bar, nkb * kBlockBytes);
             for (int j = 0; j < nkb; ++j) {
-              if (j < a.nope_blocks) tma2_load_3d(next_slot(), &a.map_k, bar, 64 * j, u.h, row + rank * 64);
-              else tma2_load_2d(next_slot(), &a.map_kr, bar, 64 * (j - a.nope_blocks), row + rank * 64);
+              if (j < a.nope_blocks) tma_load_3d(next_slot(), &a.map_k, bar, 64 * j, u.h, row);
+              else tma_load_2d(next_slot(), &a.map_kr, bar, 64 * (j - a.nope_blocks), row);
             }
             ++part;
-            if (!(good = room(kVBlocks))) break;
+            if (!(good = room(a.v_blocks))) break;
             // values past the sequence's end are zeroed before anyone reads them
-            bar = (t + 1) * kTile > u.nk ? smem_addr(&sm.raw[part % kParts]) : cluster_addr(&sm.full[part % kParts], 0);
-            mbar_arrive_expect_tx_at(bar, kVBlocks * kBlockBytes);
-            for (int j = 0; j < kVBlocks; ++j) tma2_load_3d(next_slot(), &a.map_v, bar, 64 * rank, u.h, row + 64 * j);
+            bar = (t + 1) * kTile > u.nk ? &sm.raw[part % kParts] : &sm.full[part % kParts];
+            mbar_arrive_expect_tx(bar, a.v_blocks * kBlockBytes);
+            for (int j = 0; j < a.v_blocks; ++j) tma_load_3d(next_slot(), &a.map_v, bar, 64 * j, u.h, row);
             ++part;
           }
         }
@@ -507,59 +388,26 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_mma_kernel(const __grid_co
       ok = __shfl_sync(0xffffffffu, good, 0) != 0;
     }
     if (lane == 0) {
-      // the copies that were issued land before the pair ends, whichever role gave up (the even CTA's barriers
-      // count both CTAs' copies, and both stay until the end)
-      if (rank == 0) {
-        for (uint32_t f = part > kParts ? part - kParts : 0; f < part; ++f)
-          drain_wait(&sm.full[f % kParts], (f / kParts) & 1u, kDrainNs);
-        if (busy > 0) drain_wait(&sm.q_full, (busy - 1) & 1u, kDrainNs);
-      }
-    }
-    __syncwarp();
-  } else if (warp == kUnitWarp) {
-    // ------------------------------------------------ units, found ahead by the even CTA for both
-    if (rank == 0) {
-      int64_t units = 0;
-      for (int b = lane; b < a.batch; b += 32) units += seq_units(a, b);
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) units += __shfl_xor_sync(0xffffffffu, units, o);
-      const int64_t total = units * a.H;
-      int64_t next = blockIdx.x / 2;
-      for (uint32_t un = 0;; ++un) {
-        const Unit u = find_unit(a, next, total, lane);
-        if (u.h >= 0 && lane == 0) next = static_cast<int64_t>(gridDim.x / 2) + atomicAdd(a.next_unit, 1u);
-        next = __shfl_sync(0xffffffffu, next, 0);
-        if (un >= 2 && !__all_sync(0xffffffffu, bounded_wait_cluster(&sm.unit_empty[un & 1], ((un >> 1) - 1) & 1u, wc))) break;
-        if (lane == 0) {
-          sm.unit[un & 1] = u;
-          mbar_arrive(&sm.unit_full[un & 1]);
-          const uint32_t to = cluster_addr(&sm.unit[un & 1], 1), bar = cluster_addr(&sm.unit_full[un & 1], 1);
-          st_async_v4(to, make_uint4(u.q0, u.nq, u.k0, u.nk), bar);
-          st_async_v4(to + 16, make_uint4(u.row0, u.h, 0u, 0u), bar);
-        }
-        if (u.h < 0) break;
-      }
-    } else {
-      // the odd CTA expects them
-      for (uint32_t un = 0;; ++un) {
-        if (lane == 0) mbar_arrive_expect_tx(&sm.unit_full[un & 1], sizeof(Unit));
-        if (!__all_sync(0xffffffffu, bounded_wait_cluster(&sm.unit_full[un & 1], (un >> 1) & 1u, wc))) break;
-        if (sm.unit[un & 1].h < 0) break;
-      }
+      // the copies that were issued land before the CTA ends, whichever role gave up
+      for (uint32_t f = part > kParts ? part - kParts : 0; f < part; ++f)
+        drain_wait(&sm.full[f % kParts], (f / kParts) & 1u, kDrainNs);
+      if (busy > 0) drain_wait(&sm.q_full, (busy - 1) & 1u, kDrainNs);
     }
     __syncwarp();
   } else {
     // ------------------------------------------------ zeroes behind a sequence's last values
     int vc = nkb % a.ring;                       // ring position of the unit's first V part
     uint32_t vp = 1, raw_phase = 0;
-    const int per = nkb + kVBlocks;
+    const int per = nkb + a.v_blocks;
     bool ok = true;
     for (uint32_t un = 0; ok; ++un) {
-      ok = __all_sync(0xffffffffu, bounded_wait_cluster(&sm.unit_full[un & 1], (un >> 1) & 1u, wc));
+      ok = __all_sync(0xffffffffu, bounded_wait_sleep(&sm.unit_full[un & 1], (un >> 1) & 1u, wc));
       if (!ok) break;
       const Unit u = sm.unit[un & 1];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm.unit_empty[un & 1]);
       if (u.h < 0) break;
-      const int nt = max(key_tiles(a, u, 0), key_tiles(a, u, 1));
+      const int nt = max(key_tiles<kRows>(a, u, 0), key_tiles<kRows>(a, u, 1));
       if (nt > 0 && nt * kTile > u.nk) {
         const uint32_t p = vp + 2 * (nt - 1);
         const int keep = u.nk - (nt - 1) * kTile;
@@ -567,33 +415,28 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_mma_kernel(const __grid_co
         ok = __all_sync(0xffffffffu, bounded_wait_sleep(&sm.raw[p % kParts], (raw_phase >> (p % kParts)) & 1u, wc));
         if (!ok) break;
         raw_phase ^= 1u << (p % kParts);
-        for (int j = 0; j < kVBlocks; ++j) {
+        for (int j = 0; j < a.v_blocks; ++j) {
           uint4* rows = reinterpret_cast<uint4*>(ring + s * kBlockBytes);
-          for (int x = max(keep - 64 * j, 0) * 8 + lane; x < 64 * 8; x += 32) rows[x] = make_uint4(0u, 0u, 0u, 0u);
+          for (int x = keep * 8 + lane; x < kTile * 8; x += 32) rows[x] = make_uint4(0u, 0u, 0u, 0u);
           if (++s == a.ring) s = 0;
         }
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive_release_at(cluster_addr(&sm.full[p % kParts], 0));
+        if (lane == 0) mbar_arrive(&sm.full[p % kParts]);
       }
       vc = (vc + nt * per) % a.ring;
       vp += 2 * nt;
-      __syncwarp();
-      if (lane == 0) mbar_arrive_relaxed_at(cluster_addr(&sm.unit_empty[un & 1], 0));
     }
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  // nothing of the other CTA reaches this one any more, but for the last commit's arrival, which the even CTA has seen
-  cluster_sync();
-  if (rank == 1 && threadIdx.x == 0) drain_wait(&sm.drain, 0, kDrainNs);
-  if (warp == kMmaWarp) tmem2_dealloc(tmem, 512);
-  // the last pair leaves the counters as it found them
-  if (rank == 0 && threadIdx.x == 0) {
+  if (warp == kMmaWarp) tmem_dealloc(tmem, 512);
+  // the last CTA leaves the counters as it found them
+  if (threadIdx.x == 0) {
     unsigned prev;
     asm volatile("atom.acq_rel.gpu.global.add.u32 %0, [%1], 1;" : "=r"(prev) : "l"(a.done) : "memory");
-    if (prev == gridDim.x / 2 - 1) {
+    if (prev == gridDim.x - 1) {
       *a.next_unit = 0u;
       *a.done = 0u;
     }
@@ -603,25 +446,26 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_mma_kernel(const __grid_co
 }  // namespace
 
 bool prompt_mma_layout(PromptMmaArgs* a, int num_sms, int max_smem) {
+  a->box_rows = kTile;
   a->nope_blocks = (a->d_nope + 63) / 64;
   a->rope_blocks = (a->d_rope + 63) / 64;
+  a->v_blocks = (a->d_v + 63) / 64;
   a->nope_ksteps = (a->d_nope - 64 * (a->nope_blocks - 1) + 15) / 16;
   a->rope_ksteps = (a->d_rope + 15) / 16;
-  const int nkb = a->nope_blocks + a->rope_blocks;
-  const int64_t q = 2ll * nkb * kQBlockBytes;
+  const int64_t q = 2ll * (a->nope_blocks + a->rope_blocks) * kBlockBytes;
   const int64_t room = static_cast<int64_t>(max_smem) - 1024 - q - static_cast<int64_t>(sizeof(Smem));
   a->ring = static_cast<int>(std::min<int64_t>(kMaxRing, room / kBlockBytes));
-  if (a->ring < nkb + kVBlocks) return false;
+  if (a->ring < a->nope_blocks + a->rope_blocks + a->v_blocks) return false;
   a->smem_bytes = static_cast<uint32_t>(1024 + q + a->ring * kBlockBytes + sizeof(Smem));
   const int64_t units = (static_cast<int64_t>(a->total_q) / kRows + a->batch) * a->H;
-  a->grid = 2 * static_cast<int>(std::min<int64_t>(num_sms / 2, units));
+  a->grid = static_cast<int>(std::min<int64_t>(num_sms, units));
   return true;
 }
 
 cudaError_t launch_prompt_mma(const PromptMmaArgs& a, cudaStream_t st) {
   const cudaError_t e = raise_smem_limit(reinterpret_cast<const void*>(prompt_mma_kernel), static_cast<int>(a.smem_bytes));
   if (e != cudaSuccess) return e;
-  return launch_pdl(prompt_mma_kernel, dim3(a.grid), dim3(kThreads), a.smem_bytes, st, 2, a);
+  return launch_pdl(prompt_mma_kernel, dim3(a.grid), dim3(kThreads), a.smem_bytes, st, 1, a);
 }
 
 }  // namespace li

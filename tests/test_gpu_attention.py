@@ -454,7 +454,7 @@ def check_prompt(q, kn, kr, v, cu_q, cu_k, scale, causal, out, lse):
                             f"sequence {b} query {i}")
 
 
-def run_prompt(ctx, nq, nk, H, dn, dr, dv, dt, causal=True, seed=0, pad=3, check=True):
+def run_prompt(ctx, nq, nk, H, dn, dr, dv, dt, causal=True, seed=0, pad=3, check=True, max_q=None):
     tq, tk = sum(nq) + pad, sum(nk) + pad
     q = rand(tq, H, dn + dr, dtype=dt, seed=seed, scale=2.0).to(DEV)
     kv = rand(tk, H, dn + dv, dtype=dt, seed=seed + 1).to(DEV)
@@ -470,7 +470,7 @@ def run_prompt(ctx, nq, nk, H, dn, dr, dv, dt, causal=True, seed=0, pad=3, check
     lse = torch.full((tq, H), 3.0, device=DEV)
     ws = li.attention_workspace(ctx, H, dv)
     scale = (dn + dr) ** -0.5
-    li.li_prompt_attention(ctx, q, kn, kr, v, i32(cu_q), i32(cu_k), max(max(nq), 1), scale, out, ws, lse=lse, causal=causal)
+    li.li_prompt_attention(ctx, q, kn, kr, v, i32(cu_q), i32(cu_k), max_q or max(max(nq), 1), scale, out, ws, lse=lse, causal=causal)
     assert li.li_device_status(ctx, ws) == "LI_OK"
     assert (out[cu_q[-1]:] == 3).all() and (lse[cu_q[-1]:] == 3).all(), "rows behind the last sequence changed"
     if check:
@@ -497,6 +497,24 @@ def test_prompt_attention(ctx, case, dt):
 
 def test_prompt_attention_long(ctx):
     run_prompt(ctx, [1500, 3, 2100], [1500, 700, 2100], 2, 128, 64, 128, BF)
+
+
+@pytest.mark.parametrize("case", PA, ids=[f"q{max(c[0])}k{max(c[1])}b{len(c[0])}h{c[2]}d{c[3]}r{c[4]}v{c[5]}{'c' if c[6] else 'f'}" for c in PA])
+def test_prompt_attention_small_sequences_by_pairs(ctx, case):
+    """max_q above every sequence's queries: short sequences by the kernel for long ones."""
+    nq, nk, H, dn, dr, dv, causal = case
+    run_prompt(ctx, nq, nk, H, dn, dr, dv, BF, causal, pad=2100, max_q=2100)
+
+
+@pytest.mark.parametrize("n", [2048, 2049, 2561], ids=lambda n: f"n{n}")
+def test_prompt_attention_where_the_kernel_changes(ctx, n):
+    run_prompt(ctx, [n, 1], [n + 77, 2], 2, 128, 64, 128, BF)
+
+
+def test_prompt_attention_many_short_sequences(ctx):
+    nq = [(7 * i) % 5 for i in range(150)]
+    run_prompt(ctx, nq, [n + i % 3 for i, n in enumerate(nq)], 2, 64, 32, 64, BF)
+    run_prompt(ctx, nq, [n + i % 3 for i, n in enumerate(nq)], 2, 64, 32, 64, BF, pad=2100, max_q=2100)
 
 
 def test_prompt_attention_clamps_offsets(ctx):
