@@ -13,8 +13,9 @@
 // fit next to the queries (2 x 72 KB + 72 KB at 576 x 64): one is loaded while
 // the other is worked on.  With one tile of 128 tokens the loads waited for
 // the products and the products for the loads: 10,200 cycles a tile of 128
-// against 5,000 of MMA, 189 us for 4 x 131072 rows.  Cost of the small tile:
-// the scores' MMAs run at M = 64, 32 cycles for half the tokens (48 at M = 128).
+// against 5,000 of MMA, 189 us for 4 x 131072 rows, against 152 us now.  Cost
+// of the small tile: the scores' MMAs run at M = 64, 32 cycles for half the
+// tokens (48 at M = 128).
 //
 // The running maximum m is kept per head and moves only when a score exceeds
 // it by more than 8 (in powers of two): then weights stay below 256 and
@@ -730,6 +731,7 @@ __global__ void __launch_bounds__(kThreads, 1) latent_mma_kernel(const __grid_co
       for (int p = 0; p < parts; ++p)
         drain_wait(&sm.full[i % a.bufs][p], static_cast<uint32_t>(i / a.bufs) & 1u, kDrainNs);
     if (lw == 0 && queries > 0) drain_wait(&sm.q_full, (queries - 1) & 1u, kDrainNs);
+    if (!ok) delay_ns(kDrainNs);                 // a first part whose second was not loaded
   }
   tc_fence_before();
   __syncthreads();
@@ -744,7 +746,10 @@ __global__ void __launch_bounds__(128) latent_join_kernel(const __grid_constant_
   pdl_begin();
   const int4 cut = a.cuts[blockIdx.x];            // first row, rows, first CTA, last CTA
   const int c = blockIdx.y, lane = threadIdx.x & 31;
-  if (c >= cut.y) return;
+  // after a wait that ran out, a group may have left no entry
+  if (c >= cut.y || cut.x < 0 || cut.x + static_cast<int64_t>(cut.y) > static_cast<int64_t>(a.seqs) * a.rows || cut.z < 0 ||
+      cut.w >= a.grid)
+    return;
   const int64_t i0 = cut.z, i1 = cut.w;
   auto slot = [&](int64_t i) { return 2 * i + (i == i0 ? 1 : 0); };
   const int d = threadIdx.x * 4;

@@ -71,3 +71,69 @@ def test_follower_gather_wait_that_runs_out_is_reported_and_the_context_recovers
         assert np.isfinite(fd[0, 0, :cn]).all()
     finally:
         ctx.close()
+
+
+@pytest.mark.parametrize("case", [([300] * 3, 1), ([20000], 1), ([200, 4000], 5)], ids=["groups", "split", "queries"])
+def test_latent_attention_wait_that_runs_out_is_reported_and_the_context_recovers(case):
+    """The attention kernels; the call before leaves the workspace with entries of other sizes."""
+    lens, T = case
+    ctx = li.Context(0)
+    try:
+        ws = li.attention_workspace(ctx, 16, 512)
+        rng = torch.Generator().manual_seed(5)
+
+        def call(lens, T):
+            b, pages = len(lens), (max(lens) + 63) // 64
+            data = torch.randn(b * pages, 64, 576, generator=rng).bfloat16().to(DEV)
+            table = torch.arange(b * pages, dtype=torch.int32, device=DEV).view(b, pages)
+            cache = li.PagedCache(data, table, torch.tensor(lens, dtype=torch.int32, device=DEV))
+            q = torch.randn(b, T, 16, 576, generator=rng).bfloat16().to(DEV)
+            out = torch.zeros(b, T, 16, 512, dtype=torch.bfloat16, device=DEV)
+            return out, lambda: li.li_latent_attention(ctx, cache, q, 512, 0.04, out, ws)
+
+        _, large = call([700] * 40, 3)
+        out, run = call(lens, T)
+        run()
+        good = out.clone()
+        large()
+        li.li_set_wait_limit(ctx, 0)
+        try:
+            run()
+            st = li.li_device_status(ctx, ws)
+        finally:
+            li.li_set_wait_limit(ctx, 2_000_000_000)
+        assert st == "LI_ERR_DEVICE_TIMEOUT"
+        run()
+        assert li.li_device_status(ctx, ws) == "LI_OK"
+        assert torch.equal(out, good) and torch.isfinite(out).all()
+    finally:
+        ctx.close()
+
+
+@pytest.mark.parametrize("nq", [[300, 40], [2200, 5]], ids=["single", "pair"])
+def test_prompt_attention_wait_that_runs_out_is_reported_and_the_context_recovers(nq):
+    ctx = li.Context(0)
+    try:
+        n, H = sum(nq), 4
+        rng = torch.Generator().manual_seed(6)
+        q, kn, v, kr = (torch.randn(*s, generator=rng).bfloat16().to(DEV) for s in ((n, H, 192), (n, H, 128), (n, H, 128), (n, 64)))
+        cu = torch.tensor([0, nq[0], n], dtype=torch.int32, device=DEV)
+        ws = li.attention_workspace(ctx, H, 128)
+        out = torch.zeros(n, H, 128, dtype=torch.bfloat16, device=DEV)
+        run = lambda: li.li_prompt_attention(ctx, q, kn, kr, v, cu, cu, max(nq), 0.07, out, ws)  # noqa: E731
+        run()
+        good = out.clone()
+        li.li_set_wait_limit(ctx, 0)
+        try:
+            run()
+            st = li.li_device_status(ctx, ws)
+        finally:
+            li.li_set_wait_limit(ctx, 2_000_000_000)
+        assert st == "LI_ERR_DEVICE_TIMEOUT"
+        for _ in range(2):
+            out.zero_()
+            run()
+            assert li.li_device_status(ctx, ws) == "LI_OK"
+            assert torch.equal(out, good)
+    finally:
+        ctx.close()
