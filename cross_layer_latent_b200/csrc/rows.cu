@@ -84,6 +84,13 @@ __device__ __forceinline__ Raw8<T> load_raw8(const T* p) {
   for (int i = 0; i < static_cast<int>(sizeof(T) / 2); ++i) r.u[i] = reinterpret_cast<const uint4*>(p)[i];
   return r;
 }
+// The same to shared memory, by copies that the lane waits for.
+template <typename T>
+__device__ __forceinline__ void copy_raw8(Raw8<T>* to, const T* p) {
+#pragma unroll
+  for (int i = 0; i < static_cast<int>(sizeof(T) / 2); ++i)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_addr(&to->u[i])), "l"(reinterpret_cast<const uint4*>(p) + i) : "memory");
+}
 __device__ __forceinline__ void unpack8(const Raw8<float>& r, float (&v)[8]) {
 #pragma unroll
   for (int e = 0; e < 8; ++e) v[e] = reinterpret_cast<const float*>(&r)[e];
@@ -289,7 +296,7 @@ __device__ __forceinline__ void transform_smem(float* row, int lane, const li_ro
 
 // Two warps a block: a token's tasks are few (17 for 64 + 1 heads of 192), and
 // what a warp sets up for a set pays from several tasks on (256 threads: 183 us
-// for 8192 tokens, 128: 125, 64: 106).
+// for 8192 tokens, 128: 125, 64: 106, before rows came through shared memory).
 constexpr int kVecThreads = 64;
 constexpr int kAnyWarps = 4;
 
@@ -381,11 +388,16 @@ __global__ void __launch_bounds__(kVecThreads) norm_rope_vec_kernel(const __grid
 // The common kind of head rows: RMS norm without beta or no norm, rotary chunks
 // in one register row.  What a lane needs of the parameters and angles then
 // stays in its registers for all tasks of a set, and a row costs little more
-// than its arithmetic (170 instructions a task of four rows of 192 against
-// 620 of the general kernel).
-template <typename T, int NC, int LPR, int ROPE>
-__device__ __forceinline__ void plain_set(const li_head_rows& s, int64_t tok, const float2* tab, int t0, int t1, int l, int g) {
+// than its arithmetic.  Registers leave 20 warps to an SM, so each keeps the rows
+// of several tasks on their way, in shared memory (one task, in registers, and
+// 16 warps: 104 us for 8192 x 65 rows of 192, most of them waiting for loads).
+constexpr int kAhead = 3, kSlots = kAhead + 1;
+template <typename T, int NC, int LPR, int ROPE, typename Angles>
+__device__ __forceinline__ void plain_set(const li_head_rows& s, int64_t tok, const float2* tab, int t0, int t1, int l, int g,
+                                          Raw8<T> (*ring)[NC][32], Angles angles) {
   constexpr int G = 32 / LPR, kWarps = kVecThreads / 32;
+  const int lane = threadIdx.x & 31;
+  int at = 0;
   const li_row_transform& tf = s.tf;
   const bool normed = tf.norm != LI_NORM_NONE;
   const int n0 = tf.norm_offset / 8, n1 = normed ? n0 + tf.norm_dim / 8 : n0;
@@ -400,6 +412,20 @@ __device__ __forceinline__ void plain_set(const li_head_rows& s, int64_t tok, co
     for (int e = 0; e < 8; ++e) gamma[j][e] = 1.f;
     if (in_norm[j] && tf.gamma) load_params(tf.gamma + (c - n0) * 8, gamma[j]);
   }
+  const T* x = static_cast<const T*>(s.x) + tok * s.tok_stride + l * 8;
+  int task = t0 + (threadIdx.x >> 5);
+  // the rows of the next kAhead tasks are on their way to shared memory, each lane's chunks by its own copies
+  auto load = [&](int n) {
+    const int h = (task + n * kWarps) * G + g;
+#pragma unroll
+    for (int j = 0; j < NC; ++j)
+      if (task + n * kWarps < t1 && h < s.H && in_row[j]) copy_raw8(&ring[(at + n) % kSlots][j][lane], x + h * s.head_stride + LPR * 8 * j);
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+#pragma unroll
+  for (int n = 0; n < kAhead; ++n) load(n);
+  angles();                                      // the block's, if this is its first set
+  if (task >= t1) return;
   // rotary chunks are register row j0 of lanes [first, first + nc)
   const int r0 = tf.rope_offset / 8, nc = tf.rope_dim / 8, hc = nc / 2, j0 = r0 / LPR;
   const int rc = l - (r0 - j0 * LPR);
@@ -418,25 +444,15 @@ __device__ __forceinline__ void plain_set(const li_head_rows& s, int64_t tok, co
     }
   }
   const float inv_n = normed ? __frcp_rn(static_cast<float>(tf.norm_dim)) : 0.f;
-  const T* x = static_cast<const T*>(s.x) + tok * s.tok_stride + l * 8;
   T* out = static_cast<T*>(s.out) + tok * s.out_tok_stride + l * 8;
-  int task = t0 + (threadIdx.x >> 5);
-  if (task >= t1) return;
-  Raw8<T> next[NC];
-  auto load = [&](int h) {
-#pragma unroll
-    for (int j = 0; j < NC; ++j) {
-      next[j] = Raw8<T>{};
-      if (h < s.H && in_row[j]) next[j] = load_raw8(x + h * s.head_stride + LPR * 8 * j);
-    }
-  };
-  load(task * G + g);
   for (; task < t1; task += kWarps) {
+    asm volatile("cp.async.wait_group %0;" ::"n"(kAhead - 1) : "memory");
     const int h = task * G + g;
     Raw8<T> raw[NC];
 #pragma unroll
-    for (int j = 0; j < NC; ++j) raw[j] = next[j];
-    if (task + kWarps < t1) load(h + kWarps * G);   // on its way while this one is worked on
+    for (int j = 0; j < NC; ++j) raw[j] = ring[at][j][lane];
+    load(kAhead);                                // to the slot that was read one task ago
+    at = (at + 1) % kSlots;
     float r = 1.f;
     if (normed) {
       float ss = 0.f;
@@ -463,24 +479,32 @@ __device__ __forceinline__ void plain_set(const li_head_rows& s, int64_t tok, co
 #pragma unroll
         for (int e = 0; e < 8; ++e) w[e] = ROPE == 1 ? v[e ^ 1] : __shfl_sync(0xffffffffu, v[e], src, LPR);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] = fmaf(si[e], w[e], co[e] * v[e]);
+        for (int e = 0; e < 8; ++e) v[e] = in ? fmaf(si[e], w[e], co[e] * v[e]) : v[e];
       }
       if (h < s.H && in_row[j]) store8(o + LPR * 8 * j, v);
     }
   }
 }
 
+// Ten blocks an SM where 96 registers hold a lane's part (8192 x 65 rows of 192:
+// 82 us, 85 with eight blocks of 121 registers, 87 with twelve that spill).
 template <typename T, int NC, int LPR>
-__global__ void __launch_bounds__(kVecThreads) norm_rope_plain_kernel(const __grid_constant__ NormRopeArgs a) {
+__global__ void __launch_bounds__(kVecThreads, sizeof(T) == 2 && NC <= 3 ? 10 : 6) norm_rope_plain_kernel(const __grid_constant__ NormRopeArgs a) {
   pdl_begin();
   pdl_release();
   extern __shared__ float2 tab[];                // [n_sets][tab_stride]
+  __shared__ Raw8<T> rings[kVecThreads / 32][kSlots][NC][32];
   constexpr int G = 32 / LPR;
   const int64_t tok = blockIdx.x / a.blocks;
   const int b0 = static_cast<int>(blockIdx.x - tok * a.blocks) * a.per_block, b1 = min(b0 + a.per_block, a.tasks);
   const int l = threadIdx.x % LPR, g = (threadIdx.x & 31) / LPR;
-  fill_tables<T>(a, tok, tab);
-  __syncthreads();
+  bool filled = false;
+  auto angles = [&]() {
+    if (filled) return;
+    fill_tables<T>(a, tok, tab);
+    __syncthreads();
+    filled = true;
+  };
   int first = 0;                                 // first task of the set
   for (int i = 0; i < a.n_sets; ++i) {
     const li_head_rows& s = a.set[i];
@@ -488,9 +512,9 @@ __global__ void __launch_bounds__(kVecThreads) norm_rope_plain_kernel(const __gr
     first += n;
     if (t0 >= t1) continue;
     const float2* t = tab + table_of(a, i) * a.tab_stride;
-    if (s.tf.rope_dim == 0) plain_set<T, NC, LPR, 0>(s, tok, t, t0, t1, l, g);
-    else if (!s.tf.rope_halves) plain_set<T, NC, LPR, 1>(s, tok, t, t0, t1, l, g);
-    else plain_set<T, NC, LPR, 2>(s, tok, t, t0, t1, l, g);
+    if (s.tf.rope_dim == 0) plain_set<T, NC, LPR, 0>(s, tok, t, t0, t1, l, g, rings[threadIdx.x >> 5], angles);
+    else if (!s.tf.rope_halves) plain_set<T, NC, LPR, 1>(s, tok, t, t0, t1, l, g, rings[threadIdx.x >> 5], angles);
+    else plain_set<T, NC, LPR, 2>(s, tok, t, t0, t1, l, g, rings[threadIdx.x >> 5], angles);
   }
 }
 
