@@ -70,6 +70,7 @@ class GroupIndexer:
             self.cand = torch.full((batch, T, B), -1, dtype=torch.int32, device=dev)
             self.cand_n = torch.zeros(batch, T, dtype=torch.int32, device=dev)
         self.ws = workspace(ctx, batch, T, capacity, H, k, B or 0, device=dev)
+        self._attn_workspaces = {}               # by size
 
     # ------------------------------------------------------------ loading a prefix
     def load(self, lengths, W_K, q, w, latent=None, hidden=None, W_down=None, q_pos=None, dsa_keys=True):
@@ -202,11 +203,14 @@ class GroupIndexer:
         """The layer's latent attention over the tokens it selected last
         (idx[layer]): absorbed queries q [batch, T, heads, dim] over the layer's
         own paged latents, out [batch, T, heads, d_v].  The heads are the
-        attention's, not the indexer's.  Its workspace is made by the first
-        call (make that call before any capture) and grows with the heads."""
+        attention's, not the indexer's.  The workspace of a size (ws_attn: the
+        last call's) is made by the first call that needs it (make that call
+        before any capture) and stays for the group's life, since captured
+        graphs may hold it; calls on several streams need ordering."""
         need = li_attention_workspace_bytes(self.ctx, q.shape[2], d_v)
-        if not hasattr(self, "ws_attn") or self.ws_attn.numel() < need:
-            self.ws_attn = attention_workspace(self.ctx, q.shape[2], d_v, device=self.device)
+        self.ws_attn = self._attn_workspaces.get(need)
+        if self.ws_attn is None:
+            self.ws_attn = self._attn_workspaces[need] = attention_workspace(self.ctx, q.shape[2], d_v, device=self.device)
         li_latent_attention(self.ctx, cache, q, d_v, scale, out, self.ws_attn, lse=lse, sel=self.idx[layer],
                             q_pos=self.q_pos, stream=stream)
         return out

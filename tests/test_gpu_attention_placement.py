@@ -2,6 +2,8 @@
 a tensor, two streams, and captured graphs, each with its own workspace.  Results
 are compared with the same call at an ordinary place, bit for bit (no result
 depends on where its operands lie or on what runs beside it)."""
+import weakref
+
 import pytest
 import torch
 
@@ -140,3 +142,26 @@ def test_two_graphs_with_a_workspace_each(ctx):
     for (_, outs, ws), g in zip(pairs, good):
         assert li.li_device_status(ctx, ws) == "LI_OK"
         assert all(torch.equal(a, b) for a, b in zip(outs, g))
+
+
+def test_a_captured_attend_outlives_a_wider_one(ctx):
+    """A graph of the group's attention keeps its workspace when a later call needs a larger one."""
+    G = li.GroupIndexer(ctx, batch=1, capacity=512, d_c=64, H=8, d_k=64, G=1, k=300)
+    G.idx[0].copy_(i32(list(range(300))).view(1, 1, -1))
+    n = 400
+    data = rand(8, 64, 576, seed=50)
+    cache = li.PagedCache(data, torch.arange(8, dtype=torch.int32, device=DEV)[None].contiguous(), i32([n]))
+    q = rand(1, 1, 16, 576, seed=51)
+    out = torch.empty(1, 1, 16, 64, dtype=BF, device=DEV)
+    G.attend(0, cache, q, 64, 0.04, out)
+    torch.cuda.synchronize()
+    good, held = out.clone(), weakref.ref(G.ws_attn)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        G.attend(0, cache, q, 64, 0.04, out)
+    G.attend(0, cache, q, 512, 0.04, torch.empty(1, 1, 16, 512, dtype=BF, device=DEV))
+    assert held() is not None
+    out.zero_()
+    g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out, good)
