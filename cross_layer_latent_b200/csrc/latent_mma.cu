@@ -47,7 +47,6 @@ constexpr int kMmaWarp = kSoftWarps;
 constexpr int kLookWarp = kMmaWarp + 1;           // finds the pool rows of tiles ahead
 constexpr int kLoadWarps = 4;
 constexpr int kLook = 4;                         // tiles that it may be ahead (a power of two)
-constexpr int kHalf = 4;                         // blocks of a tile's first part; the rest is the second
 constexpr int kThreads = 32 * (kSoftWarps + 2 + kLoadWarps);
 constexpr int kMaxBufs = 4;
 constexpr int kMaxSlots = 9;
@@ -56,8 +55,7 @@ constexpr float kNoMax = -1e30f;
 constexpr uint64_t kDrainNs = 1000ull * 1000ull;
 
 struct Smem {
-  uint64_t full[kMaxBufs][2];                    // part of a tile arrived
-  uint64_t empty[kMaxBufs][2];                   // it is free again
+  uint64_t full[kMaxBufs], empty[kMaxBufs];      // a tile arrived, is free again
   uint64_t look_full[kLook], look_empty[kLook];  // pool rows of a tile's tokens
   uint64_t q_full, q_empty, s_full[2], p_full[2], pv_done, o_full, o_empty, drain;
   uint32_t tmem;
@@ -235,15 +233,12 @@ __global__ void __launch_bounds__(kThreads, 1) latent_mma_kernel(const __grid_co
   const uint32_t tiles_smem = q_smem + a.nb * N * 128;
   Smem& sm = *reinterpret_cast<Smem*>(base + a.nb * N * 128 + static_cast<size_t>(a.bufs) * a.slots * kBlockBytes);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int parts = a.slots > kHalf ? 2 : 1;
   const WaitCtl wc{&sm.abort_flag, a.status, a.wait_ns};
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < a.bufs; ++i) {
-      for (int j = 0; j < parts; ++j) {
-        mbar_init(&sm.full[i][j], 32 * kLoadWarps);
-        mbar_init(&sm.empty[i][j], 1);
-      }
+      mbar_init(&sm.full[i], 32 * kLoadWarps);
+      mbar_init(&sm.empty[i], 1);
     }
     for (int i = 0; i < kLook; ++i) {
       mbar_init(&sm.look_full[i], 1);
@@ -506,44 +501,37 @@ __global__ void __launch_bounds__(kThreads, 1) latent_mma_kernel(const __grid_co
         if (seg > 0 && !(ok = bounded_wait(&sm.o_empty, (seg - 1) & 1u, wc))) break;
         const int nt = w.s.t1 - w.s.t0;
         // One step at a time, so that each kind's code stays small and warm: the products with the values as
-        // soon as the weights are there, else the next tile's scores, part by part, as far as the tile is here.
-        int st = 0, part = 0, vt = 0;            // tiles whose scores are issued, parts of the next, tiles done
+        // soon as the weights are there, else the next tile's scores once it is here.  (Tiles in two to four parts,
+        // each loaded and freed by itself, gained nothing and cost up to a tenth.)
+        int st = 0, vt = 0;                      // tiles whose scores are issued, tiles done
         uint64_t idle = cycles();
         while (vt < nt) {
           if (vt < st && mbar_test_wait(&sm.p_full[vsr.buf], vsr.ph)) {
             tc_fence_after();
             const uint32_t v = v0 + vr.buf * tile_step, pt = v + (a.slots - 1) * kBlockStep;
-            uint64_t* const empty = sm.empty[vr.buf];
-            for (int mb = 0; mb < a.m_blocks; ++mb) {
+            for (int mb = 0; mb < a.m_blocks; ++mb)
               umma_ss_steps<kTile / 16, 128, 128>(o_tmem + mb * N, v + 2 * mb * kBlockStep, pt, id_o, vt > 0 ? 1u : 0u);
-              if (2 * (mb + 1) == kHalf && parts == 2 && mb < a.m_blocks - 1) umma_commit(&empty[0]);
-            }
-            if (parts == 1 || 2 * a.m_blocks <= kHalf) umma_commit(&empty[0]);
-            if (parts == 2) umma_commit(&empty[1]);
+            umma_commit(&sm.empty[vr.buf]);
             umma_commit(&sm.pv_done);
             vr.step(a.bufs);
             vsr.step(a.s_bufs);
             if (++vt == nt) umma_commit(&sm.o_full);
-          } else if (st < nt && st < vt + a.s_bufs && mbar_test_wait(&sm.full[sr.buf][part], sr.ph)) {
+          } else if (st < nt && st < vt + a.s_bufs && mbar_test_wait(&sm.full[sr.buf], sr.ph)) {
             fence_proxy_async_smem();            // rows gathered by cp.async are read by the tensor cores
             tc_fence_after();
             const uint32_t d = s_tmem + ssr.buf * N;
-            const int end = part == 0 ? min(kHalf, a.nb) : a.nb;
-            uint32_t c = c0 + sr.buf * tile_step + part * kHalf * kBlockStep, q = q0 + part * kHalf * kQStep;
-            for (int j = part * kHalf; j < end; ++j, c += kBlockStep, q += kQStep) {
+            uint32_t c = c0 + sr.buf * tile_step, q = q0;
+            for (int j = 0; j < a.nb; ++j, c += kBlockStep, q += kQStep) {
               if (j < a.nb - 1 || a.last_ksteps == 4) {
                 umma_ss_steps<4, 2, 2>(d, c, q, id_s, j > 0 ? 1u : 0u);
               } else {
                 for (int k = 0; k < a.last_ksteps; ++k) umma_ss_steps<1, 2, 2>(d, c + 2 * k, q + 2 * k, id_s, j + k > 0 ? 1u : 0u);
               }
             }
-            if (++part == parts) {
-              umma_commit(&sm.s_full[ssr.buf]);
-              sr.step(a.bufs);
-              ssr.step(a.s_bufs);
-              part = 0;
-              if (++st == nt) umma_commit(&sm.q_empty);
-            }
+            umma_commit(&sm.s_full[ssr.buf]);
+            sr.step(a.bufs);
+            ssr.step(a.s_bufs);
+            if (++st == nt) umma_commit(&sm.q_empty);
           } else {
             if (!*wc.abort_flag && cycles() - idle <= a.wait_ns * kCyclesPerNs) continue;
             ok = give_up(wc);
@@ -693,45 +681,38 @@ __global__ void __launch_bounds__(kThreads, 1) latent_mma_kernel(const __grid_co
         __syncwarp();
         if (lane == 0) mbar_arrive(&sm.look_empty[lk]);
         const uint32_t dst = tiles_smem + buf * a.slots * kBlockBytes;
-        for (int p = 0; p < parts; ++p) {
-          const int end = p == 0 ? min(kHalf, a.nb) : a.nb;
-          if (tile >= a.bufs) ok = __all_sync(0xffffffffu, bounded_wait(&sm.empty[buf][p], free_phase, wc));
-          if (!ok) break;
-          if (boxes) {
-            // blocks p * kHalf + lw, + 4, ... are this warp's
-            const int first = p * kHalf + lw;
-            const int mine = first < end ? (end - first + kLoadWarps - 1) / kLoadWarps : 0;
-            if (lane == 0) {
-              mbar_arrive_n(&sm.full[buf][p], 31);
-              mbar_arrive_expect_tx(&sm.full[buf][p], mine * kBlockBytes);
-            }
-            if (lane < per)
-              for (int j = first; j < end; j += kLoadWarps)
-                tma_load_2d(base + (dst - q_smem) + j * kBlockBytes + at * 128, &a.map_box, &sm.full[buf][p], 64 * j, box_row);
-          } else {
-            for (int j = p * kHalf; j < end; ++j) {
-              const bool in_row = 64 * j + c * 8 < a.dim;
-#pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                // tokens that nobody attends, and columns past the row, become zeros
-                const bool on = in_row && ((there >> i) & 1u);
-                cp_async_16_or_zero(dst + (i & 1 ? odd : even) + j * kBlockBytes + i * 512,
-                                    on ? src[i] + j * 128 : static_cast<const uint8_t*>(a.data), on ? 16u : 0u);
-              }
-            }
-            cp_async_arrive_noinc(&sm.full[buf][p]);
-          }
-        }
+        if (tile >= a.bufs) ok = __all_sync(0xffffffffu, bounded_wait(&sm.empty[buf], free_phase, wc));
         if (!ok) break;
+        if (boxes) {
+          // blocks lw, lw + 4, ... are this warp's
+          const int mine = lw < a.nb ? (a.nb - lw + kLoadWarps - 1) / kLoadWarps : 0;
+          if (lane == 0) {
+            mbar_arrive_n(&sm.full[buf], 31);
+            mbar_arrive_expect_tx(&sm.full[buf], mine * kBlockBytes);
+          }
+          if (lane < per)
+            for (int j = lw; j < a.nb; j += kLoadWarps)
+              tma_load_2d(base + (dst - q_smem) + j * kBlockBytes + at * 128, &a.map_box, &sm.full[buf], 64 * j, box_row);
+        } else {
+          for (int j = 0; j < a.nb; ++j) {
+            const bool in_row = 64 * j + c * 8 < a.dim;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              // tokens that nobody attends, and columns past the row, become zeros
+              const bool on = in_row && ((there >> i) & 1u);
+              cp_async_16_or_zero(dst + (i & 1 ? odd : even) + j * kBlockBytes + i * 512,
+                                  on ? src[i] + j * 128 : static_cast<const uint8_t*>(a.data), on ? 16u : 0u);
+            }
+          }
+          cp_async_arrive_noinc(&sm.full[buf]);
+        }
       }
     }
     // the copies that were issued land before the CTA ends, whichever role gave up
     cp_async_wait_all();
     for (int64_t i = max(tile - a.bufs, int64_t(0)); i < tile; ++i)
-      for (int p = 0; p < parts; ++p)
-        drain_wait(&sm.full[i % a.bufs][p], static_cast<uint32_t>(i / a.bufs) & 1u, kDrainNs);
+      drain_wait(&sm.full[i % a.bufs], static_cast<uint32_t>(i / a.bufs) & 1u, kDrainNs);
     if (lw == 0 && queries > 0) drain_wait(&sm.q_full, (queries - 1) & 1u, kDrainNs);
-    if (!ok) delay_ns(kDrainNs);                 // a first part whose second was not loaded
   }
   tc_fence_before();
   __syncthreads();
