@@ -694,16 +694,21 @@ __global__ void __launch_bounds__(kThreads, 1) latent_mma_kernel(const __grid_co
             for (int j = lw; j < a.nb; j += kLoadWarps)
               tma_load_2d(base + (dst - q_smem) + j * kBlockBytes + at * 128, &a.map_box, &sm.full[buf], 64 * j, box_row);
         } else {
-          for (int j = 0; j < a.nb; ++j) {
-            const bool in_row = 64 * j + c * 8 < a.dim;
+          // tokens that nobody attends, and columns past the row, become zeros
+          uint32_t n[4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              // tokens that nobody attends, and columns past the row, become zeros
-              const bool on = in_row && ((there >> i) & 1u);
-              cp_async_16_or_zero(dst + (i & 1 ? odd : even) + j * kBlockBytes + i * 512,
-                                  on ? src[i] + j * 128 : static_cast<const uint8_t*>(a.data), on ? 16u : 0u);
-            }
+          for (int i = 0; i < 4; ++i) n[i] = (there >> i) & 1u ? 16u : 0u;
+          uint32_t to = dst + even, to_odd = dst + odd;
+#pragma unroll 4
+          for (int j = 0; j < a.nb - 1; ++j, to += kBlockBytes, to_odd += kBlockBytes) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) cp_async_16_or_zero((i & 1 ? to_odd : to) + i * 512, src[i] + j * 128, n[i]);
           }
+          const bool in_row = 64 * (a.nb - 1) + c * 8 < a.dim;
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            cp_async_16_or_zero((i & 1 ? to_odd : to) + i * 512, in_row ? src[i] + (a.nb - 1) * 128 : static_cast<const uint8_t*>(a.data),
+                                in_row ? n[i] : 0u);
           cp_async_arrive_noinc(&sm.full[buf]);
         }
       }
