@@ -570,6 +570,8 @@ constexpr int kAppendLanes = 16;
 // workspace, which that block resets).
 // PLAIN: RMS or no norm and pairs or no rotation, the one body of
 // transform_kind that covers those.
+// 4 x 8192 rows of 576 take 19 us (4 TB/s read and written), bound by the chain
+// of loads start, page, row; one row each of 8 sequences 7 us.
 template <typename T, int NC, bool PLAIN>
 __global__ void __launch_bounds__(kAnyWarps * 32) append_paged_kernel(const __grid_constant__ AppendPagedArgs a) {
   pdl_begin();
