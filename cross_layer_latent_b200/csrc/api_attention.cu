@@ -41,9 +41,13 @@ li_status check_attn_ws(li_ctx* c, const void* ws, size_t bytes, size_t need, co
   return LI_OK;
 }
 
-// Checks a row transform for rows of `dim` elements; *chunked tells whether
-// its ranges suit the wide path (whole chunks of 8).
-li_status check_transform(li_ctx* c, const li_row_transform& tf, int dim, bool* chunked, const char* what) {
+// Checks a row transform for rows of `dim` elements and copies it to *out
+// without the fields of parts that are switched off, which the kernels then
+// need not tell from parts that are on (an off part is an empty range);
+// *chunked tells whether its ranges suit the wide path (whole chunks of 8).
+li_status check_transform(li_ctx* c, const li_row_transform& tf, int dim, li_row_transform* out, bool* chunked, const char* what) {
+  memset(out, 0, sizeof(*out));
+  out->norm = LI_NORM_NONE;
   if (tf.norm != LI_NORM_NONE && tf.norm != LI_NORM_RMS && tf.norm != LI_NORM_LAYER)
     return fail(c, LI_ERR_ARG, "%s: unknown norm %d", what, static_cast<int>(tf.norm));
   if (tf.norm != LI_NORM_NONE) {
@@ -52,6 +56,12 @@ li_status check_transform(li_ctx* c, const li_row_transform& tf, int dim, bool* 
     if (!(tf.eps >= 0.f) || !std::isfinite(tf.eps)) return fail(c, LI_ERR_ARG, "%s: eps must be finite and >= 0", what);
     if (!aligned(tf.gamma, 4) || !aligned(tf.beta, 4)) return fail(c, LI_ERR_ALIGN, "%s: gamma and beta must be 4-byte aligned", what);
     if (tf.norm_offset % 8 || tf.norm_dim % 8) *chunked = false;
+    out->norm = tf.norm;
+    out->norm_offset = tf.norm_offset;
+    out->norm_dim = tf.norm_dim;
+    out->gamma = tf.gamma;
+    out->beta = tf.beta;
+    out->eps = tf.eps;
   }
   if (tf.rope_dim != 0) {
     if (tf.rope_dim < 2 || tf.rope_dim % 2 || tf.rope_offset < 0 || tf.rope_offset > dim - tf.rope_dim)
@@ -62,6 +72,10 @@ li_status check_transform(li_ctx* c, const li_row_transform& tf, int dim, bool* 
     if (!aligned(tf.inv_freq, 4)) return fail(c, LI_ERR_ALIGN, "%s: inv_freq must be 4-byte aligned", what);
     if (tf.rope_offset % 8 || tf.rope_dim % 8) *chunked = false;
     if (tf.rope_halves && tf.rope_dim % 16) *chunked = false;
+    out->rope_offset = tf.rope_offset;
+    out->rope_dim = tf.rope_dim;
+    out->rope_halves = tf.rope_halves;
+    out->inv_freq = tf.inv_freq;
   }
   return LI_OK;
 }
@@ -104,24 +118,24 @@ li_status norm_rope(li_ctx* c, const li_head_rows* sets, int n_sets, li_dtype dt
     if (r.H < 1 || r.dim < 1 || r.dim > kMaxRowDim)
       return fail(c, LI_ERR_SHAPE, "%s: need H >= 1 and dim in [1, %d]", what, kMaxRowDim);
     if (!aligned(r.x, eb) || !aligned(r.out, eb)) return fail(c, LI_ERR_ALIGN, "%s: x and out must be aligned to their elements", what);
-    if ((s = check_transform(c, r.tf, r.dim, &vec, what)) != LI_OK) return s;
+    a.set[i] = r;
+    if ((s = check_transform(c, r.tf, r.dim, &a.set[i].tf, &vec, what)) != LI_OK) return s;
     if (n_tok > 0 && r.tf.rope_dim && !pos) return fail(c, LI_ERR_ARG, "%s: a rotation needs pos", what);
     if (r.dim % 8 || !aligned(r.x, 16) || !aligned(r.out, 16) || r.tok_stride % 8 || r.head_stride % 8 ||
         r.out_tok_stride % 8 || r.out_head_stride % 8)
       vec = false;
     max_dim = std::max(max_dim, r.dim);
     heads += r.H;
-    a.set[i] = r;
   }
   if (pos && !aligned(pos, 4)) return fail(c, LI_ERR_ALIGN, "%s: pos must be 4-byte aligned", what);
   if (heads > 65535) return fail(c, LI_ERR_SHAPE, "%s: more than 65535 heads", what);
   if (n_tok == 0) return LI_OK;
   a.n_sets = n_sets;
   a.pos = pos;
-  const NormRopePlan plan = plan_norm_rope(sets, n_sets, vec, max_dim);
+  const NormRopePlan plan = plan_norm_rope(a.set, n_sets, vec, max_dim);
   for (int i = 0; i < n_sets; ++i) {
     a.tasks += (sets[i].H + plan.rows - 1) / plan.rows;
-    a.tab_stride = std::max(a.tab_stride, (sets[i].tf.rope_dim / 2 + 1) / 2 * 2);
+    a.tab_stride = std::max(a.tab_stride, (a.set[i].tf.rope_dim / 2 + 1) / 2 * 2);
   }
   // A block takes all of a token's tasks (its angles once) when the tokens
   // alone fill the GPU, else one a warp.
@@ -153,10 +167,7 @@ li_status append_paged(li_ctx* c, const li_paged_cache* cache, const void* x, in
   AppendPagedArgs a;
   memset(&a, 0, sizeof(a));
   bool vec = cache->dim % 8 == 0;
-  if (tf) {
-    if ((s = check_transform(c, *tf, cache->dim, &vec, what)) != LI_OK) return s;
-    a.tf = *tf;
-  }
+  if (tf && (s = check_transform(c, *tf, cache->dim, &a.tf, &vec, what)) != LI_OK) return s;
   vec = vec && append_in_chunks(a.tf, cache->dim);
   if ((s = check_attn_ws(c, ws, ws_bytes, kAttnHeader, what)) != LI_OK) return s;
   if ((s = check_device(c, what)) != LI_OK) return s;
