@@ -3,6 +3,7 @@
 
 #include <cuda.h>
 #include <cuda_runtime.h>
+#include <math.h>
 #include <stdint.h>
 
 #include "../../include/li.h"
@@ -49,6 +50,15 @@ cudaError_t launch_norm_rope(const NormRopeArgs& a, li_dtype dtype, const NormRo
 cudaError_t launch_append_paged(const AppendPagedArgs& a, li_dtype dtype, bool vec, int num_sms, cudaStream_t st);
 
 // ---- attention
+
+// What a row's sum of weights l makes of it: the factor of its output and its
+// log-sum-exp, `log_sum` where there are weights.  l = 0: nothing attended, or
+// only scores of -inf, so out = 0 and lse = -inf.  l is NaN where a score was NaN
+// or +inf, and stays so.
+#ifdef __CUDACC__
+__device__ __forceinline__ float inverse_sum(float l) { return l > 0.f ? 1.f / l : l; }
+__device__ __forceinline__ float row_lse(float l, float log_sum) { return l > 0.f ? log_sum : (l == 0.f ? -INFINITY : l); }
+#endif
 
 struct LatentAttnArgs {
   const float* q;

@@ -75,7 +75,8 @@ __device__ __forceinline__ void attend(const float* q, int d1, int d2, int d_v, 
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
     const float now = fmaxf(m, top);
-    if (now == -INFINITY) continue;
+    // fmaxf passes over a NaN: such a score goes on, and makes the row's sums NaN
+    if (now == -INFINITY && !__any_sync(0xffffffffu, z != z)) continue;
     const float keep = expf(m - now), p = expf(z - now);
     m = now;
     s = fmaf(s, keep, p);                        // a lane's own share of the sum
@@ -132,14 +133,14 @@ __device__ __forceinline__ void attend(const float* q, int d1, int d2, int d_v, 
     w[i] = pm[i] == -INFINITY ? 0.f : expf(pm[i] - M);
     L = fmaf(w[i], pl[i], L);
   }
-  const float inv = L > 0.f ? 1.f / L : 0.f;
+  const float inv = inverse_sum(L);
   for (int i = threadIdx.x; i < d_v; i += kWarps * 32) {
     float x = 0.f;
 #pragma unroll
     for (int u = 0; u < kWarps; ++u) x = fmaf(w[u], part[u][i], x);
     out[i] = x * inv;
   }
-  if (lse && threadIdx.x == 0) *lse = L > 0.f ? M + logf(L) : -INFINITY;
+  if (lse && threadIdx.x == 0) *lse = row_lse(L, M + logf(L));
 }
 
 // One block per (sequence, query, head).

@@ -272,14 +272,22 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
   return r;
 }
 
+// The larger of two values, NaN if either is.
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
 // 2^x of a pair on the FMA pipes, for x <= 100: x = n + r with |r| <= 1/2, a
 // polynomial for 2^r and n added to its exponent.  The coefficients are the
 // best of degree 4 for the relative error on [-1/2, 1/2] (a Remez exchange):
 // 2.7e-6, 4e-8 on average, a two-hundredth of the rounding to bf16 that
-// follows.  x below -126 counts as -126.
+// follows.  x below -126 counts as -126.  NaN gives 3.4e38: the exponent that is
+// added to the canonical NaN 0x7FFFFFFF is its own lowest bits.
 __device__ __forceinline__ float2 exp2_poly(uint64_t x) {
   float2 v = unpair(x);
-  const uint64_t y = pair(fmaxf(v.x, -126.f), fmaxf(v.y, -126.f));
+  const uint64_t y = pair(max_nan(v.x, -126.f), max_nan(v.y, -126.f));
   const uint64_t big = pair(12582912.f, 12582912.f), less = pair(-12582912.f, -12582912.f);   // 1.5 * 2^23: rounds to whole
   const uint64_t n = add2(y, big);
   const uint64_t whole = add2(n, less);

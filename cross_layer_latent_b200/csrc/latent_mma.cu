@@ -447,9 +447,9 @@ __global__ void __launch_bounds__(kThreads, 1) latent_mma_kernel(const __grid_co
       if (threadIdx.x % 128 < CW) {
         const int c = c0 + threadIdx.x % 128;
         const float l = sm.part[0][c] + sm.part[1][c] + sm.part[2][c] + sm.part[3][c];
-        sm.alpha[c] = whole ? (l > 0.f ? 1.f / l : 0.f) : 1.f;
+        sm.alpha[c] = whole ? inverse_sum(l) : 1.f;
         if (whole) {
-          if (a.lse && c < rows) a.lse[row0 + c] = l > 0.f ? (sm.m[c] + log2f(l)) * 0.69314718056f : -INFINITY;
+          if (a.lse && c < rows) a.lse[row0 + c] = row_lse(l, (sm.m[c] + log2f(l)) * 0.69314718056f);
         } else {
           a.part_ml[(slot * 64 + c) * 2] = sm.m[c];
           a.part_ml[(slot * 64 + c) * 2 + 1] = l;
@@ -775,13 +775,13 @@ __global__ void __launch_bounds__(128) latent_join_kernel(const __grid_constant_
     }
   }
   const int64_t row = static_cast<int64_t>(cut.x) + c;
-  const float inv = L > 0.f ? 1.f / L : 0.f;
+  const float inv = inverse_sum(L);
   const float v[4] = {s.x * inv, s.y * inv, s.z * inv, s.w * inv};
   __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out) + row * a.d_v + d;
 #pragma unroll
   for (int e = 0; e < 4; ++e)
     if (d + e < a.d_v) out[e] = __float2bfloat16_rn(v[e]);
-  if (threadIdx.x == 0 && a.lse) a.lse[row] = L > 0.f ? (M + log2f(L)) * 0.69314718056f : -INFINITY;
+  if (threadIdx.x == 0 && a.lse) a.lse[row] = row_lse(L, (M + log2f(L)) * 0.69314718056f);
 }
 
 template <int N>

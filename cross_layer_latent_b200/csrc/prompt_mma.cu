@@ -203,7 +203,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_mma_kernel(const __grid_co
         ++outs;
         tc_fence_after();
       }
-      const float inv = l > 0.f ? 1.f / l : 0.f;
+      const float inv = inverse_sum(l);
       const int64_t row = static_cast<int64_t>(u.q0 + i) * a.H + u.h;
       for (int c = 0; c < a.d_v; c += 32) {
         uint32_t o[32];
@@ -221,7 +221,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_mma_kernel(const __grid_co
           store_row32(static_cast<__nv_bfloat16*>(a.out) + row * a.d_v + c, w, a.d_v - c, a.wide_out);
         }
       }
-      if (a.lse && i < u.nq) a.lse[row] = l > 0.f ? (m * a.scale_log2 + log2f(l)) * 0.69314718056f : -INFINITY;
+      if (a.lse && i < u.nq) a.lse[row] = row_lse(l, (m * a.scale_log2 + log2f(l)) * 0.69314718056f);
       if (n > 0) {
         tc_fence_before();
         __syncwarp();

@@ -30,6 +30,8 @@
 // The pairs are persistent and take units (prompt_units.cuh) from a counter
 // that the even CTA draws on for both (dealt out in turn, the slowest pair had
 // 20% more work).
+#include <math_constants.h>
+
 #include <algorithm>
 
 #include "attention.h"
@@ -227,7 +229,6 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_pair_kernel(const __grid_c
       if (lane == 0) mbar_arrive_relaxed_at(u_bar[un & 1]);   // the unit's numbers have been used
       if (u.row0 + q * kPairRows >= u.nq) continue;
       // the row's sum: both halves, after the last tile's maxima have been read
-      if (lim <= 0) l = 0.f;                     // nothing to attend
       named_bar_sync(bar, 64);
       sm.part[q][half][r] = l;
       ok = n == 0 || bounded_wait(&sm.o_full[q], outs & 1u, wc);
@@ -236,8 +237,12 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_pair_kernel(const __grid_c
         break;
       }
       l += sm.part[q][half ^ 1][r];
+      // What exp2_poly makes of scores that are not finite shows in the sum, which is 1 or nearly, its maximum's weight,
+      // to 256 a key for a row that has a softmax.  Below: hidden keys alone, or scores that are all -inf.  Above: a NaN.
+      if (l < 0x1p-64f) l = 0.f;
+      if (m == INFINITY || l > 0x1p100f) l = CUDART_NAN_F;
       tc_fence_after();
-      const float inv = l > 0.f ? 1.f / l : 0.f;
+      const float inv = inverse_sum(l);
       const int64_t row = static_cast<int64_t>(u.q0 + i) * a.H + u.h;
       for (int c = half * my_cols; c < min((half + 1) * my_cols, a.d_v); c += 32) {
         uint32_t o[32];
@@ -255,7 +260,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_pair_kernel(const __grid_c
           store_row32(static_cast<__nv_bfloat16*>(a.out) + row * a.d_v + c, w, a.d_v - c, a.wide_out);
         }
       }
-      if (a.lse && half == 0 && i < u.nq) a.lse[row] = l > 0.f ? (m * a.scale_log2 + log2f(l)) * 0.69314718056f : -INFINITY;
+      if (a.lse && half == 0 && i < u.nq) a.lse[row] = row_lse(l, (m * a.scale_log2 + log2f(l)) * 0.69314718056f);
       if (n > 0) {
         ++outs;
         tc_fence_before();

@@ -514,7 +514,9 @@ LI_API li_status li_append_paged(li_ctx* ctx, const li_paged_cache* cache, const
  *   sel [batch][T][k] int32 (a selection output, -1 padded): its entries in
  *   [0, n_bt); negative ones are skipped, others record LI_ERR_INDEX and
  *   are skipped.  A position listed twice counts twice.
- * A query that attends nothing gets out = 0 and lse = -inf.  A page outside
+ * A query that attends nothing gets out = 0 and lse = -inf, and so does one
+ * whose scores are all -inf; a score of NaN or +inf makes out and lse of that
+ * query and head NaN.  A page outside
  * [0, n_pages) records LI_ERR_INDEX and its positions are skipped.  Rows
  * that no query attends are not read (they may hold anything); without sel,
  * rows below lengths[b] must be finite even where q_pos hides them from
