@@ -88,7 +88,8 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_pair_kernel(const __grid_c
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sm.unit_full[i], 1);
-      mbar_init(&sm.unit_empty[i], 2 * kSoftWarps + 5);   // MMA issue, and softmax, loads and zeroes of both CTAs
+      // MMA issue; softmax, loads and zeroes of both CTAs; the odd CTA's unit warp
+      mbar_init(&sm.unit_empty[i], 1 + 2 * (kSoftWarps + 2) + 1);
       mbar_init(&sm.s_full[i], 1);
       mbar_init(&sm.p_full[i], 16);
       mbar_init(&sm.o_full[i], 1);
@@ -458,6 +459,9 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_pair_kernel(const __grid_c
         if (lane == 0) mbar_arrive_expect_tx(&sm.unit_full[un & 1], sizeof(Unit));
         if (!__all_sync(0xffffffffu, bounded_wait_cluster(&sm.unit_full[un & 1], (un >> 1) & 1u, wc))) break;
         if (sm.unit[un & 1].h < 0) break;
+        // read: the unit after the next may take its place
+        __syncwarp();
+        if (lane == 0) mbar_arrive_relaxed_at(cluster_addr(&sm.unit_empty[un & 1], 0));
       }
     }
     __syncwarp();
