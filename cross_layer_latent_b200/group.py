@@ -32,6 +32,15 @@ def _cache(batch, capacity, dim, dtype, device, scale_split: int = 0) -> Cache:
                  scale_split=scale_split)
 
 
+def _as_stream(stream, device):
+    """A stream argument (None: the current stream, a torch stream or its handle) as a torch stream."""
+    if stream is None or isinstance(stream, torch.cuda.Stream):
+        return stream
+    if int(stream) == 0:
+        return torch.cuda.default_stream(device)
+    return torch.cuda.ExternalStream(int(stream), device=device)
+
+
 class GroupIndexer:
     """Buffers and calls for one group: latent cache, per-layer absorbed
     queries and selections, HS candidates, optional DSA key caches."""
@@ -210,7 +219,9 @@ class GroupIndexer:
         need = li_attention_workspace_bytes(self.ctx, q.shape[2], d_v)
         self.ws_attn = self._attn_workspaces.get(need)
         if self.ws_attn is None:
-            self.ws_attn = self._attn_workspaces[need] = attention_workspace(self.ctx, q.shape[2], d_v, device=self.device)
+            # made and zeroed on the stream that uses it, so that the zeros are there before the kernels
+            with torch.cuda.stream(_as_stream(stream, self.device)):
+                self.ws_attn = self._attn_workspaces[need] = attention_workspace(self.ctx, q.shape[2], d_v, device=self.device)
         li_latent_attention(self.ctx, cache, q, d_v, scale, out, self.ws_attn, lse=lse, sel=self.idx[layer],
                             q_pos=self.q_pos, stream=stream)
         return out
