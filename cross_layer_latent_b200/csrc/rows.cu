@@ -328,7 +328,7 @@ template <typename T, int NC, int LPR>
 __global__ void __launch_bounds__(kVecThreads) norm_rope_vec_kernel(const __grid_constant__ NormRopeArgs a) {
   pdl_begin();
   pdl_release();
-  extern __shared__ float2 tab[];                // [n_sets][tab_stride]
+  extern __shared__ __align__(16) float2 tab[];  // [n_sets][tab_stride]
   constexpr int G = 32 / LPR, kWarps = kVecThreads / 32;
   const int64_t tok = blockIdx.x / a.blocks;
   const int t0 = static_cast<int>(blockIdx.x - tok * a.blocks) * a.per_block, t1 = min(t0 + a.per_block, a.tasks);
@@ -365,18 +365,19 @@ __global__ void __launch_bounds__(kVecThreads) norm_rope_vec_kernel(const __grid
     task += kWarps;
     load();                                      // on its way while this one is worked on
     const li_head_rows& s = a.set[si];
-    const uint32_t t = smem_addr(tab + table_of(a, si) * a.tab_stride);
+    const float2* t = tab + table_of(a, si) * a.tab_stride;
     T* out = static_cast<T*>(s.out) + tok * s.out_tok_stride + head * s.out_head_stride;
     const bool there = head < s.H;
     const int dim = s.dim;
     transform_chunks<T, NC, LPR>(
         raw, l, s.tf,
         [t](int i, float2 (&o)[4]) {
+          // i is even and so is tab_stride: 16-byte loads
 #pragma unroll
           for (int k = 0; k < 4; k += 2) {
-            asm("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
-                : "=f"(o[k].x), "=f"(o[k].y), "=f"(o[k + 1].x), "=f"(o[k + 1].y)
-                : "r"(t + 8u * (i + k)));
+            const float4 two = *reinterpret_cast<const float4*>(t + i + k);
+            o[k] = make_float2(two.x, two.y);
+            o[k + 1] = make_float2(two.z, two.w);
           }
         },
         [=](int c, const float (&v)[8]) {
@@ -492,7 +493,7 @@ template <typename T, int NC, int LPR>
 __global__ void __launch_bounds__(kVecThreads, sizeof(T) == 2 && NC <= 3 ? 10 : 6) norm_rope_plain_kernel(const __grid_constant__ NormRopeArgs a) {
   pdl_begin();
   pdl_release();
-  extern __shared__ float2 tab[];                // [n_sets][tab_stride]
+  extern __shared__ __align__(16) float2 tab[];  // [n_sets][tab_stride]
   __shared__ Raw8<T> rings[kVecThreads / 32][kSlots][NC][32];
   constexpr int G = 32 / LPR;
   const int64_t tok = blockIdx.x / a.blocks;
@@ -523,7 +524,7 @@ template <typename T>
 __global__ void __launch_bounds__(kAnyWarps * 32) norm_rope_any_kernel(const __grid_constant__ NormRopeArgs a) {
   pdl_begin();
   pdl_release();
-  extern __shared__ float2 tab[];
+  extern __shared__ __align__(16) float2 tab[];
   __shared__ float rows[kAnyWarps][kMaxRowDim];
   const int64_t tok = blockIdx.x / a.blocks;
   const int t0 = static_cast<int>(blockIdx.x - tok * a.blocks) * a.per_block, t1 = min(t0 + a.per_block, a.tasks);
