@@ -164,6 +164,9 @@ li_status append_paged(li_ctx* c, const li_paged_cache* cache, const void* x, in
   const int eb = elt_bytes(cache->dtype);
   if (!aligned(x, 16) || tok_stride * eb % 16) return fail(c, LI_ERR_ALIGN, "%s: rows of x must be 16-byte aligned", what);
   if (!aligned(start, 4) || !aligned(n_new, 4)) return fail(c, LI_ERR_ALIGN, "%s: start and n_new must be 4-byte aligned", what);
+  for (const int32_t* p : {start, n_new})
+    if (p && p != cache->lengths && p < cache->lengths + cache->batch && cache->lengths < p + cache->batch)
+      return fail(c, LI_ERR_ARG, "%s: start and n_new may be the lengths, but not overlap them otherwise", what);
   AppendPagedArgs a;
   memset(&a, 0, sizeof(a));
   bool vec = cache->dim % 8 == 0;
@@ -178,6 +181,7 @@ li_status append_paged(li_ctx* c, const li_paged_cache* cache, const void* x, in
   a.lengths = cache->lengths;
   a.start = start == cache->lengths ? nullptr : start;   // the lengths themselves: they are read before they advance
   a.n_new = n_new;
+  a.lengths_last = !a.start || n_new == cache->lengths;
   a.batch = cache->batch;
   a.T = T;
   a.n_pages = cache->n_pages;

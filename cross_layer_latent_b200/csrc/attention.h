@@ -34,6 +34,7 @@ struct AppendPagedArgs {
   const int32_t* n_new;
   int batch, T, n_pages, page_size, max_pages, dim;
   li_row_transform tf;
+  int lengths_last;        // rows take their numbers from the lengths: these advance when every row has
   unsigned int* done;
   int* status;
 };

@@ -566,9 +566,9 @@ constexpr int kAppendLanes = 16;
 // faster at 576: their registers left too few rows in flight); NC = 0: any size and
 // alignment, a warp a row by way of shared memory.  Every row has a position
 // of its own, so a lane forms the angles of its own slots.  Sequence lengths
-// advance after every row's start has been read: at once when the starts
-// come from `start`, else in the last block to finish (a counter in the
-// workspace, which that block resets).
+// advance after every row's start and number have been read: at once when
+// both come from elsewhere, else in the last block to finish (a counter in
+// the workspace, which that block resets).
 // PLAIN: RMS or no norm and pairs or no rotation, the one body of
 // transform_kind that covers those (its ranges are empty where a part is off).
 // 4 x 8192 rows of 576 take 19 us (4 TB/s read and written), bound by the chain
@@ -599,7 +599,7 @@ __global__ void __launch_bounds__(kAnyWarps * 32) append_paged_kernel(const __gr
     const NewRows nr = new_rows(a, b);
     if (row && t == 0 && l == 0) {
       if (!nr.ok) record_status(a.status, kStatusCapacity);
-      else if (a.start) a.lengths[b] = static_cast<int>(nr.start) + nr.n;
+      else if (!a.lengths_last) a.lengths[b] = static_cast<int>(nr.start) + nr.n;
     }
     const bool mine = row && nr.ok && t < nr.n;
     const int pos = mine ? static_cast<int>(nr.start) + t : 0;
@@ -628,7 +628,7 @@ __global__ void __launch_bounds__(kAnyWarps * 32) append_paged_kernel(const __gr
       __syncwarp();
     }
   }
-  if (a.start) return;
+  if (!a.lengths_last) return;
   __shared__ unsigned last;
   __syncthreads();
   if (threadIdx.x == 0) {

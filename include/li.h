@@ -492,6 +492,8 @@ LI_API size_t li_attention_workspace_bytes(const li_ctx* ctx, int H, int d_v);
  *        draft, say), or NULL: s_b = lengths[b].
  * n_new  [batch] int32 device: n_b, clamped to [0, T] (padded batches), or
  *        NULL: n_b = T.
+ * start and n_new may be the lengths themselves, which are read before they
+ * advance, but must not overlap them otherwise (LI_ERR_ARG).
  * If s_b < 0 or s_b + n_b exceeds max_pages * page_size nothing is written
  * for b, lengths[b] stays, and the status word records LI_ERR_CAPACITY.  A
  * row whose page is outside [0, n_pages) is not written (LI_ERR_INDEX).
