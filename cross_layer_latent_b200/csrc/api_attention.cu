@@ -162,7 +162,8 @@ li_status append_paged(li_ctx* c, const li_paged_cache* cache, const void* x, in
   if (static_cast<int64_t>(cache->batch) * T >= (int64_t(1) << 31)) return fail(c, LI_ERR_SHAPE, "%s: batch * T too large", what);
   if (cache->dim > kMaxRowDim) return fail(c, LI_ERR_SHAPE, "%s: dim must be <= %d", what, kMaxRowDim);
   const int eb = elt_bytes(cache->dtype);
-  if (!aligned(x, 16) || tok_stride * eb % 16) return fail(c, LI_ERR_ALIGN, "%s: rows of x must be 16-byte aligned", what);
+  const bool one = static_cast<int64_t>(cache->batch) * T == 1;   // a single row has no stride to speak of
+  if (!aligned(x, 16) || (!one && tok_stride * eb % 16)) return fail(c, LI_ERR_ALIGN, "%s: rows of x must be 16-byte aligned", what);
   if (!aligned(start, 4) || !aligned(n_new, 4)) return fail(c, LI_ERR_ALIGN, "%s: start and n_new must be 4-byte aligned", what);
   for (const int32_t* p : {start, n_new})
     if (p && p != cache->lengths && p < cache->lengths + cache->batch && cache->lengths < p + cache->batch)
@@ -390,14 +391,17 @@ li_status prompt_attention(li_ctx* c, const li_prompt* p, void* out, float* lse,
   if (p->total_q > 0 && (!p->q || !out)) return fail(c, LI_ERR_ARG, "%s: q and out must be non-NULL", what);
   if (p->total_k > 0 && (!p->k_nope || !p->v || (p->d_rope && !p->k_rope)))
     return fail(c, LI_ERR_ARG, "%s: k_nope, v and (with d_rope) k_rope must be non-NULL", what);
-  if (!aligned(p->q, 16) || !aligned(p->k_nope, 16) || !aligned(p->k_rope, 16) || !aligned(p->v, 16) || !aligned(out, 16) ||
-      p->q_tok_stride % m || p->q_head_stride % m || p->k_tok_stride % m || p->k_head_stride % m || p->kr_tok_stride % m ||
-      p->v_tok_stride % m || p->v_head_stride % m)
+  if (!aligned(p->q, 16) || !aligned(p->k_nope, 16) || !aligned(p->k_rope, 16) || !aligned(p->v, 16) || !aligned(out, 16))
     return fail(c, LI_ERR_ALIGN, "%s: every row must be 16-byte aligned", what);
-  if ((p->H > 1 && (p->q_head_stride <= 0 || p->k_head_stride <= 0 || p->v_head_stride <= 0)) ||
-      (p->total_q > 1 && p->q_tok_stride <= 0) ||
-      (p->total_k > 1 && (p->k_tok_stride <= 0 || p->v_tok_stride <= 0 || (p->d_rope && p->kr_tok_stride <= 0))))
-    return fail(c, LI_ERR_ARG, "%s: strides must be positive", what);
+  // strides of dimensions of one element are never stepped
+  const struct { int64_t stride, count; } steps[] = {
+      {p->q_head_stride, p->H}, {p->k_head_stride, p->H}, {p->v_head_stride, p->H}, {p->q_tok_stride, p->total_q},
+      {p->k_tok_stride, p->total_k}, {p->v_tok_stride, p->total_k}, {p->kr_tok_stride, p->d_rope ? p->total_k : 0}};
+  for (const auto& d : steps)
+    if (d.count > 1) {
+      if (d.stride % m) return fail(c, LI_ERR_ALIGN, "%s: every row must be 16-byte aligned", what);
+      if (d.stride <= 0) return fail(c, LI_ERR_ARG, "%s: strides must be positive", what);
+    }
   if ((s = check_attn_ws(c, ws, ws_bytes, li_attention_workspace_bytes(c, p->H, p->d_v), what)) != LI_OK) return s;
   if ((s = check_device(c, what)) != LI_OK) return s;
   if (p->total_q == 0 || p->max_q == 0) return LI_OK;

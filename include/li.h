@@ -486,7 +486,8 @@ LI_API size_t li_attention_workspace_bytes(const li_ctx* ctx, int H, int d_v);
  * sequence b and t < n_b, row tf(x[b][t]) is stored at position s_b + t (the
  * position its rotation uses), then lengths[b] = s_b + n_b.
  * x      [batch][T][cache->dim] of the cache's dtype, token (b, t) at
- *        x + (b * T + t) * tok_stride elements (16-byte aligned rows).
+ *        x + (b * T + t) * tok_stride elements (16-byte aligned rows;
+ *        tok_stride may be anything where there is one).
  * tf     NULL stores the rows as they are.
  * start  [batch] int32 device: s_b (rewriting positions after a rejected
  *        draft, say), or NULL: s_b = lengths[b].
@@ -543,8 +544,9 @@ LI_API li_status li_latent_attention(li_ctx* ctx, const li_paged_cache* cache, c
  * query that attends nothing: 0 and -inf).  A sequence's keys and values must
  * be finite, also where causality hides them; rows of no sequence may hold
  * anything.
- * Strides are in elements and positive, every row 16-byte aligned; a token's
- * row of a head is contiguous.  q rows hold d_nope + d_rope elements.
+ * Strides are in elements and positive, every row 16-byte aligned (a stride
+ * over a single token or head may be anything); a token's row of a head is
+ * contiguous.  q rows hold d_nope + d_rope elements.
  * cu_q, cu_k [batch + 1] int32 device, non-decreasing from 0; values are
  * clamped to [0, total_q] and [0, total_k], and rows of out and lse outside
  * [cu_q[0], cu_q[batch]) are left as they were.  max_q: at least the longest
