@@ -352,8 +352,11 @@ li_status prompt_mma(li_ctx* c, const li_prompt& p, void* out, float* lse, void*
   a.d_rope = p.d_rope;
   a.d_v = p.d_v;
   // Pairs of CTAs halve what an SM reads of keys and values, but their units are twice as many queries and take longer
-  // to begin and end.  Measured at d 192/128 (single CTAs, pairs): 8 sequences of up to 257 x 16 heads 20, 30 us; 4 of
-  // 2048 x 32 202, 219; 1 of 4096 x 32 220, 202; 4 of up to 4096 x 16 221, 197; 1 of 8192 x 32 723, 656.
+  // to begin and end.  Measured at d 192/128, 20 calls in a row (single CTAs, pairs): 8 sequences of up to 257 x 16 heads
+  // 18, 26 us; 4 of 1500 to 2048 x 32 170, 183; 4 of 2048 x 32 197, 203; 4 of 1000 to 4096 x 16 185, 208; 1 of 4096 x 32
+  // 203, 184; 1 of 8192 x 32 637, 605.  The rule knows max_q alone, as the lengths are on the device: where few queries
+  // see many keys pairs would be up to a sixth faster (512 x 32 heads behind 16384 keys 309, 263; 2048 behind 65536
+  // 2570, 2213; one prompt of 2048 without causality 100, 92).
   const bool pair = p.max_q > 2048;
   if (!(pair ? prompt_pair_layout(&a, c->num_sms, c->max_smem_optin) : prompt_mma_layout(&a, c->num_sms, c->max_smem_optin)))
     return fail(c, LI_ERR_UNSUPPORTED, "%s: operands too large for shared memory", what);

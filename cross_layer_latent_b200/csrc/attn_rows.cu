@@ -9,6 +9,9 @@
 // dimensions keep most lanes busy.  A warp a key at a time took 33 us for 2 x 8
 // heads over 512 rows of 48 (five shuffles and a dependent load a key); this
 // takes 15.
+// No block shares what another reads, and none splits a query's keys: made for
+// small configurations.  64 heads over 8192 rows of 576 take 620 us (14 of
+// arithmetic), a prompt of 2048 x 16 heads 6.3 ms.
 #include <cmath>
 
 #include "attention.h"

@@ -413,10 +413,11 @@ typedef enum { LI_NORM_NONE = 0, LI_NORM_RMS = 1, LI_NORM_LAYER = 2 } li_norm;
  *   [rope_dim / 2] fp32, device): x' = x cos - y sin, y' = x sin + y cos.
  *   Slot p is (x[2p], x[2p+1]) with rope_halves = 0, the layout of
  *   li_append_latent_ex, and (x[p], x[p + rope_dim / 2]) with rope_halves = 1.
- *   The angle is formed exactly, modulo whole turns, before its cosine and
- *   sine are taken in fp32 (for BF16 rows to 2^-20).  Frequencies must be
- *   finite.
- * norm = LI_NORM_NONE and rope_dim = 0 switch the parts off.                */
+ *   The angle is formed modulo whole turns, off by at most 2^-31 of a turn and
+ *   2^-62 of itself, before its cosine and sine are taken in fp32 (for BF16
+ *   rows to 2^-20).  Frequencies must be finite.
+ * norm = LI_NORM_NONE and rope_dim = 0 switch the parts off, whose other
+ * fields are then not looked at.                                            */
 typedef struct {
   li_norm norm;
   int32_t norm_offset;
@@ -540,10 +541,10 @@ LI_API li_status li_latent_attention(li_ctx* ctx, const li_paged_cache* cache, c
  * -- and the value v[j][h].  The batch is ragged: sequence b has queries
  * [cu_q[b], cu_q[b+1]) and keys [cu_k[b], cu_k[b+1]).  Query i of nq attends
  * the keys j <= i + nk - nq with causal != 0 (the last query sees all nk
- * keys), all nk keys without; scale, out and lse as li_latent_attention (a
- * query that attends nothing: 0 and -inf).  A sequence's keys and values must
- * be finite, also where causality hides them; rows of no sequence may hold
- * anything.
+ * keys), all nk keys without; scale, out and lse as li_latent_attention, for
+ * queries that attend nothing and scores that are not finite too.  A
+ * sequence's keys and values must be finite, also where causality hides them;
+ * rows of no sequence may hold anything.
  * Strides are in elements and positive, every row 16-byte aligned (a stride
  * over a single token or head may be anything); a token's row of a head is
  * contiguous.  q rows hold d_nope + d_rope elements.
