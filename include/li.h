@@ -530,7 +530,8 @@ LI_API li_status li_append_paged(li_ctx* ctx, const li_paged_cache* cache, const
  * out  [batch][T][H][d_v] of the cache's dtype, contiguous.
  * lse  [batch][T][H] fp32 or NULL.
  * BF16 runs on the tensor cores: the weights p are rounded to bf16 before
- * the product with the values, their sum is not.  Results do not depend on
+ * the product with the values, their sum is not; a query whose scores all lie
+ * below -1e30, with or without scale, counts as one with scores of -inf.  Results do not depend on
  * the order in which the GPU runs the parts.                                */
 LI_API li_status li_latent_attention(li_ctx* ctx, const li_paged_cache* cache, const void* q, int T, int H, int d_v,
                               float scale, const int32_t* q_pos, const int32_t* sel, int k, void* out, float* lse,
